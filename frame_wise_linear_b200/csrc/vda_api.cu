@@ -304,6 +304,23 @@ vda_status vda_backward_workspace_size(const vda_problem* p, size_t* bytes) {
 
 namespace {
 
+vda_status check_backward_pointers(const vda_problem& p, const void* Q, const void* K, const void* V, const void* G,
+                                   const void* K_txt, const void* V_txt, const void* dO, const void* dQ,
+                                   const void* dK, const void* dV, const void* dG, const void* dK_txt,
+                                   const void* dV_txt) {
+  vda_status s = check_pointers(p, Q, K, V, G, K_txt, V_txt, dO);
+  if (s != VDA_OK) return s;
+  const void* outs[4] = {dQ, dK, dV, dG};
+  const char* names[4] = {"dQ", "dK", "dV", "dG"};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) return fail(VDA_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if (!aligned16(outs[i])) return fail(VDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (p.n_txt > 0 && (!dK_txt || !dV_txt || !aligned16(dK_txt) || !aligned16(dV_txt)))
+    return fail(VDA_ERR_INVALID_ARG, "dK_txt / dV_txt NULL or not 16-byte aligned with n_txt = %d", p.n_txt);
+  return VDA_OK;
+}
+
 vda_status backward_impl(const vda_problem* p, const void* Q, const void* K, const void* V, const void* G,
                          const void* K_txt, const void* V_txt, const void* dO, void* dQ, void* dK, void* dV,
                          void* dG, void* dK_txt, void* dV_txt, void* workspace, size_t workspace_bytes, void* stream,
@@ -311,15 +328,7 @@ vda_status backward_impl(const vda_problem* p, const void* Q, const void* K, con
   size_t need = 0;
   vda_status s = vda_backward_workspace_size(p, &need);
   if (s != VDA_OK) return s;
-  if ((s = check_pointers(*p, Q, K, V, G, K_txt, V_txt, dO)) != VDA_OK) return s;
-  const void* outs[4] = {dQ, dK, dV, dG};
-  const char* names[4] = {"dQ", "dK", "dV", "dG"};
-  for (int i = 0; i < 4; ++i) {
-    if (!outs[i]) return fail(VDA_ERR_INVALID_ARG, "%s is NULL", names[i]);
-    if (!aligned16(outs[i])) return fail(VDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
-  }
-  if (p->n_txt > 0 && (!dK_txt || !dV_txt || !aligned16(dK_txt) || !aligned16(dV_txt)))
-    return fail(VDA_ERR_INVALID_ARG, "dK_txt / dV_txt NULL or not 16-byte aligned with n_txt = %d", p->n_txt);
+  if ((s = check_backward_pointers(*p, Q, K, V, G, K_txt, V_txt, dO, dQ, dK, dV, dG, dK_txt, dV_txt)) != VDA_OK) return s;
   if (!workspace) return fail(VDA_ERR_WORKSPACE, "workspace is NULL");
   if ((uintptr_t)workspace & 255u) return fail(VDA_ERR_WORKSPACE, "workspace not 256-byte aligned");
   if (workspace_bytes < need)
@@ -415,6 +424,310 @@ vda_status vda_merge_project(const vda_merge_problem* p, const void* O_lin, cons
                            static_cast<unsigned*>(workspace), st, p->test_stall);
   if (e != cudaSuccess) return cuda_fail(e, "merge launch");
   return VDA_OK;
+}
+
+// ------------------------------------------------------------------ token operators
+namespace {
+
+bool float_type(int dt) { return dt == VDA_DTYPE_F32 || dt == VDA_DTYPE_BF16; }
+bool aligned_elem(const void* x, int dt) { return ((uintptr_t)x & (dt == VDA_DTYPE_BF16 ? 1u : 3u)) == 0; }
+constexpr int64_t kMaxStride = (1LL << 31) - 1;
+
+// A tensor that the call reads or writes: not NULL, aligned to its elements.
+vda_status check_tensor(const void* x, int dt, const char* name) {
+  if (!x) return fail(VDA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned_elem(x, dt)) return fail(VDA_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
+  return VDA_OK;
+}
+vda_status check_optional(const void* x, int dt, const char* name) {
+  return x ? check_tensor(x, dt, name) : VDA_OK;
+}
+vda_status check_stride(int64_t ld, int64_t least, const char* name) {
+  if (ld != 0 && (ld < least || ld > kMaxStride))
+    return fail(VDA_ERR_INVALID_ARG, "%s must be 0 or in [%lld, 2^31) (got %lld)", name, (long long)least, (long long)ld);
+  return VDA_OK;
+}
+
+#define VDA_CHECK(expr)                  \
+  do {                                   \
+    const vda_status s_ = (expr);        \
+    if (s_ != VDA_OK) return s_;         \
+  } while (0)
+
+vda_status check_norm(const vda_norm_problem* p) {
+  if (!p) return fail(VDA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->tokens < 0 || p->tokens > kMaxStride)
+    return fail(VDA_ERR_INVALID_ARG, "tokens must be in [0, 2^31) (got %lld)", (long long)p->tokens);
+  if (p->heads < 1 || p->D < 1)
+    return fail(VDA_ERR_INVALID_ARG, "heads and D must be >= 1 (got %d, %d)", p->heads, p->D);
+  if (p->heads > 65536 || p->D > 8192)
+    return fail(VDA_ERR_UNSUPPORTED, "heads up to 65536 and D up to 8192 are supported (got %d, %d)", p->heads, p->D);
+  if (!float_type(p->dtype) || !float_type(p->w_dtype))
+    return fail(VDA_ERR_INVALID_ARG, "dtype and w_dtype must be float32 or bfloat16 (got %d, %d)", p->dtype, p->w_dtype);
+  if (!(p->eps > 0.f) || !isfinite(p->eps))
+    return fail(VDA_ERR_INVALID_ARG, "eps must be finite and > 0 (got %g)", (double)p->eps);
+  if (p->reserved != 0) return fail(VDA_ERR_INVALID_ARG, "reserved must be 0 (got %d)", p->reserved);
+  VDA_CHECK(check_stride(p->ld_x, (int64_t)p->heads * p->D, "ld_x"));
+  return check_stride(p->ld_y, (int64_t)p->heads * p->D, "ld_y");
+}
+
+vda_status norm_backward_impl(const vda_norm_problem* p, const void* dY, const void* X, const float* mean,
+                              const float* rstd, const void* codes, const void* scales, const void* W, void* dX,
+                              float* dW, float* dbias, void* workspace, size_t workspace_bytes, void* stream,
+                              bool from_checkpoint) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_norm(p));
+  VDA_CHECK(check_optional(W, p->w_dtype, "W"));
+  VDA_CHECK(check_optional(dW, VDA_DTYPE_F32, "dW"));
+  VDA_CHECK(check_optional(dbias, VDA_DTYPE_F32, "dbias"));
+  if (p->tokens > 0) {
+    VDA_CHECK(check_tensor(dY, p->dtype, "dY"));
+    VDA_CHECK(check_tensor(dX, p->dtype, "dX"));
+    VDA_CHECK(check_tensor(rstd, VDA_DTYPE_F32, "rstd"));
+    if (from_checkpoint) {
+      if (!codes || !scales) return fail(VDA_ERR_INVALID_ARG, "codes / scales is NULL");
+    } else {
+      VDA_CHECK(check_tensor(X, p->dtype, "X"));
+      VDA_CHECK(check_tensor(mean, VDA_DTYPE_F32, "mean"));
+    }
+    if (dW || dbias) {
+      const size_t need = vda::norm_backward_workspace_bytes(*p);
+      if (!workspace) return fail(VDA_ERR_WORKSPACE, "workspace is NULL");
+      if ((uintptr_t)workspace & 255u) return fail(VDA_ERR_WORKSPACE, "workspace not 256-byte aligned");
+      if (workspace_bytes < need)
+        return fail(VDA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    }
+  }
+  cudaError_t e = vda::launch_layer_norm_backward(
+      *p, dY, X, mean, rstd, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), W, dX, dW, dbias,
+      static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
+  return VDA_OK;
+}
+
+vda_status check_rope(const vda_rope_problem* p) {
+  if (!p) return fail(VDA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->B < 0 || p->T < 0 || p->height < 0 || p->width < 0)
+    return fail(VDA_ERR_INVALID_ARG, "B, T, height, width must be >= 0 (got %d, %d, %d, %d)", p->B, p->T, p->height,
+                p->width);
+  if (p->H_q < 0 || p->H_k < 0 || (int64_t)p->H_q + p->H_k > 65535)
+    return fail(VDA_ERR_INVALID_ARG, "H_q, H_k must be >= 0 and H_q + H_k <= 65535 (got %d, %d)", p->H_q, p->H_k);
+  if (p->d < 1) return fail(VDA_ERR_INVALID_ARG, "d must be >= 1 (got %d)", p->d);
+  if (p->d > 256) return fail(VDA_ERR_UNSUPPORTED, "d up to 256 is supported (got %d)", p->d);
+  if (p->d_t < 0 || p->d_y < 0 || p->d_x < 0 || (p->d_t | p->d_y | p->d_x) & 1 ||
+      (int64_t)p->d_t + p->d_y + p->d_x > p->d)
+    return fail(VDA_ERR_INVALID_ARG, "d_t, d_y, d_x must be even, >= 0 and at most d = %d together (got %d, %d, %d)",
+                p->d, p->d_t, p->d_y, p->d_x);
+  if (!float_type(p->dtype)) return fail(VDA_ERR_INVALID_ARG, "dtype must be float32 or bfloat16 (got %d)", p->dtype);
+  if (p->layout != VDA_LAYOUT_BHTND && p->layout != VDA_LAYOUT_BTNHD)
+    return fail(VDA_ERR_INVALID_ARG, "unknown layout %d", p->layout);
+  if (p->pairing != VDA_ROPE_INTERLEAVED && p->pairing != VDA_ROPE_HALVES)
+    return fail(VDA_ERR_INVALID_ARG, "unknown pairing %d", p->pairing);
+  if (!(p->theta > 0.0) || !isfinite(p->theta))
+    return fail(VDA_ERR_INVALID_ARG, "theta must be finite and > 0 (got %g)", p->theta);
+  for (int i = 0; i < 3; ++i)
+    if (!isfinite(p->pos0[i]) || !isfinite(p->step[i]))
+      return fail(VDA_ERR_INVALID_ARG, "pos0 and step must be finite (axis %d: %g, %g)", i, p->pos0[i], p->step[i]);
+  if (p->reserved != 0) return fail(VDA_ERR_INVALID_ARG, "reserved must be 0 (got %d)", p->reserved);
+  // B * T * height * width below 2^31, without overflowing on the way.
+  int64_t tokens = p->B;
+  for (int f : {p->T, p->height, p->width}) {
+    if (f == 0) tokens = 0;
+    if (tokens > kMaxStride) break;
+    tokens *= f;
+  }
+  if (tokens > kMaxStride && p->T && p->height && p->width)
+    return fail(VDA_ERR_UNSUPPORTED, "B * T * height * width must be below 2^31");
+  const int64_t ld[4] = {p->ld_q, p->ld_k, p->ld_qr, p->ld_kr};
+  const char* names[4] = {"ld_q", "ld_k", "ld_qr", "ld_kr"};
+  for (int i = 0; i < 4; ++i) {
+    if (p->layout == VDA_LAYOUT_BHTND && ld[i] != 0)
+      return fail(VDA_ERR_INVALID_ARG, "%s must be 0 in the [B, H, N, d] layout (got %lld)", names[i], (long long)ld[i]);
+    VDA_CHECK(check_stride(ld[i], (int64_t)(i % 2 ? p->H_k : p->H_q) * p->d, names[i]));
+  }
+  return VDA_OK;
+}
+
+vda_status rope_impl(const vda_rope_problem* p, const void* Q, const void* K, const float* positions, void* Qo,
+                     void* Ko, void* stream, bool backward) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_rope(p));
+  VDA_CHECK(check_optional(positions, VDA_DTYPE_F32, "positions"));
+  if (p->B && p->T && p->height && p->width) {
+    if (p->H_q) {
+      VDA_CHECK(check_tensor(Q, p->dtype, backward ? "dQ_rot" : "Q"));
+      VDA_CHECK(check_tensor(Qo, p->dtype, backward ? "dQ" : "Q_rot"));
+    }
+    if (p->H_k) {
+      VDA_CHECK(check_tensor(K, p->dtype, backward ? "dK_rot" : "K"));
+      VDA_CHECK(check_tensor(Ko, p->dtype, backward ? "dK" : "K_rot"));
+    }
+  }
+  cudaError_t e = vda::launch_rope(*p, Q, K, positions, Qo, Ko, backward, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, backward ? "rope backward launch" : "rope launch");
+  return VDA_OK;
+}
+
+vda_status check_checkpoint(const vda_checkpoint_problem* p, const void* X, const void* codes, const void* scales) {
+  if (!p) return fail(VDA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->rows < 0 || p->rows > (1LL << 40))
+    return fail(VDA_ERR_INVALID_ARG, "rows must be in [0, 2^40] (got %lld)", (long long)p->rows);
+  if (p->D < 1) return fail(VDA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", p->D);
+  if (p->D > (1 << 24)) return fail(VDA_ERR_UNSUPPORTED, "D up to 2^24 is supported (got %d)", p->D);
+  if (p->rows > 0 && p->D >= (1LL << 46) / p->rows + ((1LL << 46) % p->rows != 0))
+    return fail(VDA_ERR_UNSUPPORTED, "rows * D must be below 2^46");
+  if (!float_type(p->dtype)) return fail(VDA_ERR_INVALID_ARG, "dtype must be float32 or bfloat16 (got %d)", p->dtype);
+  VDA_CHECK(check_stride(p->ld, p->D, "ld"));
+  if (p->rows > 0) {
+    VDA_CHECK(check_tensor(X, p->dtype, "X"));
+    if (!codes || !scales) return fail(VDA_ERR_INVALID_ARG, "codes / scales is NULL");
+  }
+  return VDA_OK;
+}
+
+// Device copies of the backward's inputs behind its own workspace.
+size_t checkpoint_backward_bytes(const vda_problem& p, size_t (&off)[6]) {
+  const Sizes z = tensor_bytes(p);
+  const size_t parts[6] = {z.q, z.k, z.v, z.g, z.kt, z.vt};
+  size_t at = vda::backward_workspace_bytes(p);
+  for (int i = 0; i < 6; ++i) {
+    off[i] = at;
+    at = vda::align_up(at + parts[i], 256);
+  }
+  return at;
+}
+
+}  // namespace
+
+vda_status vda_layer_norm(const vda_norm_problem* p, const void* X, const void* W, const void* bias, void* Y,
+                          float* mean, float* rstd, void* codes, void* scales, void* stream) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_norm(p));
+  VDA_CHECK(check_optional(W, p->w_dtype, "W"));
+  VDA_CHECK(check_optional(bias, p->w_dtype, "bias"));
+  VDA_CHECK(check_optional(mean, VDA_DTYPE_F32, "mean"));
+  VDA_CHECK(check_optional(rstd, VDA_DTYPE_F32, "rstd"));
+  if ((codes == nullptr) != (scales == nullptr))
+    return fail(VDA_ERR_INVALID_ARG, "codes and scales must both be given or both be NULL");
+  if (p->tokens > 0) {
+    VDA_CHECK(check_tensor(X, p->dtype, "X"));
+    VDA_CHECK(check_tensor(Y, p->dtype, "Y"));
+  }
+  cudaError_t e = vda::launch_layer_norm(*p, X, W, bias, Y, mean, rstd, static_cast<uint8_t*>(codes),
+                                         static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "layer norm launch");
+  return VDA_OK;
+}
+
+vda_status vda_layer_norm_from_checkpoint(const vda_norm_problem* p, const void* codes, const void* scales,
+                                          const void* W, const void* bias, void* Y, void* stream) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_norm(p));
+  VDA_CHECK(check_optional(W, p->w_dtype, "W"));
+  VDA_CHECK(check_optional(bias, p->w_dtype, "bias"));
+  if (p->tokens > 0) {
+    if (!codes || !scales) return fail(VDA_ERR_INVALID_ARG, "codes / scales is NULL");
+    VDA_CHECK(check_tensor(Y, p->dtype, "Y"));
+  }
+  cudaError_t e = vda::launch_layer_norm_from_checkpoint(*p, static_cast<const uint8_t*>(codes),
+                                                         static_cast<const uint8_t*>(scales), W, bias, Y,
+                                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "layer norm from checkpoint launch");
+  return VDA_OK;
+}
+
+vda_status vda_layer_norm_backward_workspace_size(const vda_norm_problem* p, size_t* bytes) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_norm(p));
+  if (!bytes) return fail(VDA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = vda::norm_backward_workspace_bytes(*p);
+  return VDA_OK;
+}
+
+vda_status vda_layer_norm_backward(const vda_norm_problem* p, const void* dY, const void* X, const float* mean,
+                                   const float* rstd, const void* W, void* dX, float* dW, float* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return norm_backward_impl(p, dY, X, mean, rstd, nullptr, nullptr, W, dX, dW, dbias, workspace, workspace_bytes,
+                            stream, false);
+}
+
+vda_status vda_layer_norm_backward_from_checkpoint(const vda_norm_problem* p, const void* dY, const void* codes,
+                                                   const void* scales, const float* rstd, const void* W, void* dX,
+                                                   float* dW, float* dbias, void* workspace, size_t workspace_bytes,
+                                                   void* stream) {
+  return norm_backward_impl(p, dY, nullptr, nullptr, rstd, codes, scales, W, dX, dW, dbias, workspace,
+                            workspace_bytes, stream, true);
+}
+
+vda_status vda_rope(const vda_rope_problem* p, const void* Q, const void* K, const float* positions, void* Q_rot,
+                    void* K_rot, void* stream) {
+  return rope_impl(p, Q, K, positions, Q_rot, K_rot, stream, false);
+}
+
+vda_status vda_rope_backward(const vda_rope_problem* p, const void* dQ_rot, const void* dK_rot,
+                             const float* positions, void* dQ, void* dK, void* stream) {
+  return rope_impl(p, dQ_rot, dK_rot, positions, dQ, dK, stream, true);
+}
+
+vda_status vda_checkpoint_pack(const vda_checkpoint_problem* p, const void* X, void* codes, void* scales,
+                               void* stream) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_checkpoint(p, X, codes, scales));
+  cudaError_t e = vda::launch_checkpoint_pack(*p, X, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "checkpoint pack launch");
+  return VDA_OK;
+}
+
+vda_status vda_checkpoint_unpack(const vda_checkpoint_problem* p, const void* codes, const void* scales, void* X,
+                                 void* stream) {
+  g_msg[0] = 0;
+  VDA_CHECK(check_checkpoint(p, X, codes, scales));
+  cudaError_t e = vda::launch_checkpoint_unpack(*p, static_cast<const uint8_t*>(codes),
+                                                static_cast<const uint8_t*>(scales), X,
+                                                static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "checkpoint unpack launch");
+  return VDA_OK;
+}
+
+vda_status vda_backward_from_checkpoint_workspace_size(const vda_problem* p, size_t* bytes) {
+  size_t need = 0, off[6];
+  VDA_CHECK(vda_backward_workspace_size(p, &need));
+  if (!bytes) return fail(VDA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = checkpoint_backward_bytes(*p, off);
+  return VDA_OK;
+}
+
+vda_status vda_backward_from_checkpoint(const vda_problem* p, const vda_checkpoint* in, const void* dO, void* dQ,
+                                        void* dK, void* dV, void* dG, void* dK_txt, void* dV_txt, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  size_t need = 0, off[6];
+  VDA_CHECK(vda_backward_workspace_size(p, &need));
+  if (!in) return fail(VDA_ERR_INVALID_ARG, "in is NULL");
+  const int count = p->n_txt > 0 ? 6 : 4;
+  static const char* const names[6] = {"Q", "K", "V", "G", "K_txt", "V_txt"};
+  for (int i = 0; i < count; ++i)
+    if (!in[i].codes || !in[i].scales) return fail(VDA_ERR_INVALID_ARG, "%s's codes / scales is NULL", names[i]);
+  const size_t total = checkpoint_backward_bytes(*p, off);
+  if (!workspace) return fail(VDA_ERR_WORKSPACE, "workspace is NULL");
+  if ((uintptr_t)workspace & 255u) return fail(VDA_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  if (workspace_bytes < total)
+    return fail(VDA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, total);
+  // The remaining pointers are checked before anything is enqueued, too.
+  char* ws = static_cast<char*>(workspace);
+  void* x[6];
+  for (int i = 0; i < 6; ++i) x[i] = i < count ? ws + off[i] : nullptr;
+  VDA_CHECK(check_backward_pointers(*p, x[0], x[1], x[2], x[3], x[4], x[5], dO, dQ, dK, dV, dG, dK_txt, dV_txt));
+  const int64_t tokens = (int64_t)p->B * p->H * p->T * p->n, text = (int64_t)p->B * p->H * p->n_txt;
+  for (int i = 0; i < count; ++i) {
+    const vda_checkpoint_problem q = {i < 4 ? tokens : text, 0, 128, VDA_DTYPE_BF16};
+    cudaError_t e = vda::launch_checkpoint_unpack(q, static_cast<const uint8_t*>(in[i].codes),
+                                                  static_cast<const uint8_t*>(in[i].scales), x[i],
+                                                  static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "checkpoint unpack launch");
+  }
+  return backward_impl(p, x[0], x[1], x[2], x[3], x[4], x[5], dO, dQ, dK, dV, dG, dK_txt, dV_txt, workspace,
+                       need, stream, false);
 }
 
 vda_status vda_sync_status(void* workspace, void* stream) {

@@ -1,0 +1,175 @@
+// Device helpers of the token operators (layer norm, rotary positions, 8-bit
+// checkpoints): typed vector loads and stores, and the 8-bit block format.
+//
+// 8-bit block format.  A row's elements fall into blocks of 32 (the last one
+// may be short).  A block stores e4m3 codes (1 sign, 4 exponent, 3 mantissa
+// bits, largest finite 448) and one byte s = e + 127, where e >= -127 is the
+// least integer with max |x| <= 448 * 2^e over the block's finite values; a
+// code is x * 2^-e rounded to nearest even.  The scale is a power of two, so
+// that scaling is exact both ways and an element is rounded once, by at most
+// 2^-4 of its value (or 2^-10 * 2^e where that is more: below 2^-6 * 2^e the
+// codes are equally spaced); a scale that is not a power of two would win
+// nothing back but the last binade of the range.  NaN and infinities become
+// NaN and do not count for the scale, so the rest of their block stays.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace vda {
+namespace tokops {
+
+constexpr int kBlock = 32;   // elements that share a scale
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <int Bytes>
+struct RawOf;
+template <> struct RawOf<2> { using type = uint16_t; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<16> { using type = uint4; };
+
+// VE consecutive elements of type T as they are stored: one load or store of
+// VE * sizeof(T) bytes (2 to 16), whose address is a multiple of that.
+template <typename T, int VE>
+struct Pack {
+  using Raw = typename RawOf<VE * (int)sizeof(T)>::type;
+  union {
+    Raw raw;
+    T e[VE];
+  };
+  __device__ Pack() {}
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) e[i] = from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
+  __device__ __forceinline__ void set(int i, float x) { e[i] = from_f32<T>(x); }
+};
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// |x| where x is finite, else 0: what an element adds to its block's maximum.
+__device__ __forceinline__ float block_mag(float x) { return finite(x) ? fabsf(x) : 0.f; }
+
+// The scale byte of a block whose largest finite magnitude is `top`: top =
+// m 2^k (1 <= m < 2) needs e = k - 8 while m <= 1.75 (448 = 1.75 * 2^8), one
+// more above.  Subnormal and zero `top` take e = -127.
+__device__ __forceinline__ int scale_byte(float top) {
+  const uint32_t b = __float_as_uint(top);
+  const int s = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return s < 0 ? 0 : s;
+}
+// 2^(s - 127) and 2^(127 - s), both exact (s = 0: the subnormal 2^-127).
+__device__ __forceinline__ float scale_of(int s) { return __uint_as_float(s ? (uint32_t)s << 23 : 0x400000u); }
+__device__ __forceinline__ float inv_scale_of(int s) { return __uint_as_float((uint32_t)(254 - s) << 23); }
+
+// Two scaled values to two codes (x in the low byte).  At the largest scale
+// byte, 247, a scaled value of 248 or more would round to 256, which stands
+// for 2^128: 240 is taken, within the same half step of 2^-4.
+__device__ __forceinline__ uint32_t encode2(float x, float y, float inv, int s) {
+  x = finite(x) ? x * inv : __uint_as_float(0x7fffffffu);
+  y = finite(y) ? y * inv : __uint_as_float(0x7fffffffu);
+  if (s >= 247) {
+    x = x > 240.f ? 240.f : (x < -240.f ? -240.f : x);
+    y = y > 240.f ? 240.f : (y < -240.f ? -240.f : y);
+  }
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+// The values of two codes, unscaled (exact).
+__device__ __forceinline__ float2 decode2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The largest of v over groups of `lanes` neighbouring lanes (a power of two
+// up to 32); every lane of the warp takes part.
+template <int Lanes>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// VE values to codes, and the block's scale byte, by the 32 / VE neighbouring
+// lanes that hold the block (values beyond the row are 0).
+template <int VE>
+__device__ __forceinline__ int encode_block(const float (&x)[VE], uint8_t (&codes)[VE]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) top = fmaxf(top, block_mag(x[i]));
+  top = lanes_max<kBlock / VE>(top);
+  const int s = scale_byte(top);
+  const float inv = inv_scale_of(s);
+  if (VE == 1) {
+    codes[0] = (uint8_t)encode2(x[0], 0.f, inv, s);
+  } else {
+#pragma unroll
+    for (int i = 0; i + 1 < VE; i += 2) {
+      const uint32_t two = encode2(x[i], x[i + 1], inv, s);
+      codes[i] = (uint8_t)two;
+      codes[i + 1] = (uint8_t)(two >> 8);
+    }
+  }
+  return s;
+}
+
+// VE codes in one store or load (VE 1, 4 or 8 bytes, aligned to that).
+template <int VE>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint8_t (&c)[VE]) {
+  if constexpr (VE == 8) {
+    uint2 r;
+    r.x = c[0] | c[1] << 8 | c[2] << 16 | (uint32_t)c[3] << 24;
+    r.y = c[4] | c[5] << 8 | c[6] << 16 | (uint32_t)c[7] << 24;
+    *reinterpret_cast<uint2*>(p) = r;
+  } else if constexpr (VE == 4) {
+    *reinterpret_cast<uint32_t*>(p) = c[0] | c[1] << 8 | c[2] << 16 | (uint32_t)c[3] << 24;
+  } else {
+    static_assert(VE == 1, "1, 4 or 8 codes");
+    *p = c[0];
+  }
+}
+
+// The codes of VE neighbouring elements as loaded; values() scales them.
+template <int VE>
+struct CodePack {
+  uint32_t w[VE > 4 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (VE == 8) {
+      const uint2 r = *reinterpret_cast<const uint2*>(p);
+      w[0] = r.x;
+      w[1] = r.y;
+    } else if constexpr (VE == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(VE == 1, "1, 4 or 8 codes");
+      w[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void values(float scale, float (&x)[VE]) const {
+    if constexpr (VE == 1) {
+      x[0] = decode2(w[0]).x * scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; i += 2) {
+        const float2 v = decode2((w[i / 4] >> (8 * (i % 4))) & 0xffffu);
+        x[i] = v.x * scale;
+        x[i + 1] = v.y * scale;
+      }
+    }
+  }
+};
+
+}  // namespace tokops
+}  // namespace vda

@@ -34,6 +34,10 @@ VDA_DTYPE_E4M3 = 2     # 8-bit float inputs with per-tensor scales (uint8 storag
 VDA_LAYOUT_BHTND = 0   # Q, K, V, G, O: [B, H, T, n, d]; text [B, H, n_txt, d]
 VDA_LAYOUT_BTNHD = 1   # Q, K, V, G, O: [B, T*n, H, d]; text [B, n_txt, H, d] (bf16 only)
 
+VDA_ROPE_INTERLEAVED = 0   # a pair is two neighbouring channels
+VDA_ROPE_HALVES = 1        # channels i and i + half the turned width
+CHECKPOINT_BLOCK = 32      # neighbours of a row that share a scale byte
+
 # Testing hook for the device timeout path (vda_problem.test_stall): the wait
 # named here runs out in the first CTA of its kernel (include/vda.h).
 TEST_STALL_SITES = {
@@ -55,6 +59,17 @@ SYMBOLS = (
     "vda_backward_from_forward",
     "vda_local_softmax",
     "vda_merge_project",
+    "vda_layer_norm",
+    "vda_layer_norm_from_checkpoint",
+    "vda_layer_norm_backward_workspace_size",
+    "vda_layer_norm_backward",
+    "vda_layer_norm_backward_from_checkpoint",
+    "vda_rope",
+    "vda_rope_backward",
+    "vda_checkpoint_pack",
+    "vda_checkpoint_unpack",
+    "vda_backward_from_checkpoint_workspace_size",
+    "vda_backward_from_checkpoint",
     "vda_sync_status",
     "vda_status_string",
     "vda_last_error",
@@ -73,6 +88,30 @@ class vda_problem(ctypes.Structure):
 class vda_merge_problem(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("K", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("test_stall", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class vda_norm_problem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class vda_rope_problem(ctypes.Structure):
+    _fields_ = [("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_qr", ctypes.c_int64),
+                ("ld_kr", ctypes.c_int64), ("theta", ctypes.c_double), ("pos0", ctypes.c_double * 3),
+                ("step", ctypes.c_double * 3), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("height", ctypes.c_int32), ("width", ctypes.c_int32), ("H_q", ctypes.c_int32),
+                ("H_k", ctypes.c_int32), ("d", ctypes.c_int32), ("d_t", ctypes.c_int32), ("d_y", ctypes.c_int32),
+                ("d_x", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class vda_checkpoint_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ld", ctypes.c_int64), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class vda_checkpoint(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class VdaError(RuntimeError):
@@ -124,6 +163,20 @@ def load(path: str | None = None):
         lib.vda_merge_project.argtypes = [ctypes.POINTER(vda_merge_problem), vp, vp, vp, vp, vp, vp, ctypes.c_size_t,
                                           vp]
         lib.vda_merge_project.restype = st
+        N, R, C = (ctypes.POINTER(t) for t in (vda_norm_problem, vda_rope_problem, vda_checkpoint_problem))
+        sz = ctypes.POINTER(ctypes.c_size_t)
+        for name, args in (("vda_layer_norm", [N] + [vp] * 9),
+                           ("vda_layer_norm_from_checkpoint", [N] + [vp] * 6),
+                           ("vda_layer_norm_backward_workspace_size", [N, sz]),
+                           ("vda_layer_norm_backward", [N] + [vp] * 9 + [ctypes.c_size_t, vp]),
+                           ("vda_layer_norm_backward_from_checkpoint", [N] + [vp] * 9 + [ctypes.c_size_t, vp]),
+                           ("vda_rope", [R] + [vp] * 6), ("vda_rope_backward", [R] + [vp] * 6),
+                           ("vda_checkpoint_pack", [C] + [vp] * 4), ("vda_checkpoint_unpack", [C] + [vp] * 4),
+                           ("vda_backward_from_checkpoint_workspace_size", [P, sz]),
+                           ("vda_backward_from_checkpoint",
+                            [P, ctypes.POINTER(vda_checkpoint)] + [vp] * 8 + [ctypes.c_size_t, vp])):
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, st
         lib.vda_sync_status.argtypes = [vp, vp]
         lib.vda_sync_status.restype = st
         lib.vda_status_string.argtypes = [st]
@@ -311,6 +364,134 @@ def vda_merge_project(tokens, K, D, O_lin, W_lin, O_sm, W_sm, Y, workspace, stre
                                  _ptr(workspace), wb, _stream(stream))
     if check:
         _check(s, "vda_merge_project")
+    return s
+
+
+# ---------------------------------------------------------------------------
+# Token operators: layer norm, rotary positions, 8-bit checkpoints
+# ---------------------------------------------------------------------------
+
+def make_norm_problem(tokens, D, dtype, heads=1, w_dtype=VDA_DTYPE_F32, eps=1e-6, ld_x=0, ld_y=0) -> vda_norm_problem:
+    return vda_norm_problem(tokens, ld_x, ld_y, heads, D, dtype, w_dtype, eps, 0)
+
+
+def make_rope_problem(B, T, height, width, H_q, H_k, d, axes, dtype, layout=VDA_LAYOUT_BHTND,
+                      pairing=VDA_ROPE_INTERLEAVED, theta=10000.0, pos0=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0),
+                      ld_q=0, ld_k=0, ld_qr=0, ld_kr=0) -> vda_rope_problem:
+    """`axes` = (d_t, d_y, d_x): the channels that turn by time, height and width."""
+    d_t, d_y, d_x = axes
+    vec = ctypes.c_double * 3
+    return vda_rope_problem(ld_q, ld_k, ld_qr, ld_kr, theta, vec(*pos0), vec(*step), B, T, height, width, H_q, H_k, d,
+                            d_t, d_y, d_x, dtype, layout, pairing, 0)
+
+
+def make_checkpoint_problem(rows, D, dtype, ld=0) -> vda_checkpoint_problem:
+    return vda_checkpoint_problem(rows, ld, D, dtype)
+
+
+def vda_layer_norm(problem, X, W, bias, Y, mean=None, rstd=None, codes=None, scales=None, stream=None,
+                   check=True) -> int:
+    """Y = (X - mean) rstd W + bias per row; codes and scales: the normalised rows as an 8-bit checkpoint."""
+    s = load().vda_layer_norm(ctypes.byref(problem), _ptr(X), _ptr(W), _ptr(bias), _ptr(Y), _ptr(mean), _ptr(rstd),
+                              _ptr(codes), _ptr(scales), _stream(stream))
+    if check:
+        _check(s, "vda_layer_norm")
+    return s
+
+
+def vda_layer_norm_from_checkpoint(problem, codes, scales, W, bias, Y, stream=None, check=True) -> int:
+    """Y again from the checkpoint that vda_layer_norm left."""
+    s = load().vda_layer_norm_from_checkpoint(ctypes.byref(problem), _ptr(codes), _ptr(scales), _ptr(W), _ptr(bias),
+                                              _ptr(Y), _stream(stream))
+    if check:
+        _check(s, "vda_layer_norm_from_checkpoint")
+    return s
+
+
+def vda_layer_norm_backward_workspace_size(problem: vda_norm_problem) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().vda_layer_norm_backward_workspace_size(ctypes.byref(problem), ctypes.byref(out)),
+           "vda_layer_norm_backward_workspace_size")
+    return out.value
+
+
+def vda_layer_norm_backward(problem, dY, X, mean, rstd, W, dX, dW, dbias, workspace, stream=None,
+                            workspace_bytes=None, check=True) -> int:
+    """dX, dW, dbias (the last two float32, either may be None) of sum(dY * Y)."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    s = load().vda_layer_norm_backward(ctypes.byref(problem), _ptr(dY), _ptr(X), _ptr(mean), _ptr(rstd), _ptr(W),
+                                       _ptr(dX), _ptr(dW), _ptr(dbias), _ptr(workspace), wb, _stream(stream))
+    if check:
+        _check(s, "vda_layer_norm_backward")
+    return s
+
+
+def vda_layer_norm_backward_from_checkpoint(problem, dY, codes, scales, rstd, W, dX, dW, dbias, workspace, stream=None,
+                                            workspace_bytes=None, check=True) -> int:
+    """As vda_layer_norm_backward, from the 8-bit checkpoint of the normalised rows instead of X and mean."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    s = load().vda_layer_norm_backward_from_checkpoint(ctypes.byref(problem), _ptr(dY), _ptr(codes), _ptr(scales),
+                                                       _ptr(rstd), _ptr(W), _ptr(dX), _ptr(dW), _ptr(dbias),
+                                                       _ptr(workspace), wb, _stream(stream))
+    if check:
+        _check(s, "vda_layer_norm_backward_from_checkpoint")
+    return s
+
+
+def vda_rope(problem, Q, K, positions, Q_rot, K_rot, stream=None, check=True) -> int:
+    """Q, K turned by their positions over (time, height, width); positions: float32 [B, N, 3], or None (the grid)."""
+    s = load().vda_rope(ctypes.byref(problem), _ptr(Q), _ptr(K), _ptr(positions), _ptr(Q_rot), _ptr(K_rot),
+                        _stream(stream))
+    if check:
+        _check(s, "vda_rope")
+    return s
+
+
+def vda_rope_backward(problem, dQ_rot, dK_rot, positions, dQ, dK, stream=None, check=True) -> int:
+    """The gradients with respect to Q, K from those with respect to Q_rot, K_rot."""
+    s = load().vda_rope_backward(ctypes.byref(problem), _ptr(dQ_rot), _ptr(dK_rot), _ptr(positions), _ptr(dQ),
+                                 _ptr(dK), _stream(stream))
+    if check:
+        _check(s, "vda_rope_backward")
+    return s
+
+
+def vda_checkpoint_pack(problem, X, codes, scales, stream=None, check=True) -> int:
+    """X [rows, D] as e4m3 codes and a power-of-two scale byte per 32 neighbours of a row."""
+    s = load().vda_checkpoint_pack(ctypes.byref(problem), _ptr(X), _ptr(codes), _ptr(scales), _stream(stream))
+    if check:
+        _check(s, "vda_checkpoint_pack")
+    return s
+
+
+def vda_checkpoint_unpack(problem, codes, scales, X, stream=None, check=True) -> int:
+    """The values that codes and scales stand for, in the problem's type."""
+    s = load().vda_checkpoint_unpack(ctypes.byref(problem), _ptr(codes), _ptr(scales), _ptr(X), _stream(stream))
+    if check:
+        _check(s, "vda_checkpoint_unpack")
+    return s
+
+
+def vda_backward_from_checkpoint_workspace_size(problem: vda_problem) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().vda_backward_from_checkpoint_workspace_size(ctypes.byref(problem), ctypes.byref(out)),
+           "vda_backward_from_checkpoint_workspace_size")
+    return out.value
+
+
+def vda_backward_from_checkpoint(problem, checkpoints, dO, dQ, dK, dV, dG, dK_txt, dV_txt, workspace, stream=None,
+                                 workspace_bytes=None, check=True) -> int:
+    """vda_backward with Q, K, V, G, K_txt, V_txt given as (codes, scales) pairs (the last two may be None)."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    pairs = [(None, None) if c is None else c for c in checkpoints]
+    if len(pairs) != 6:
+        raise ValueError("checkpoints holds six entries: Q, K, V, G, K_txt, V_txt")
+    arr = (vda_checkpoint * 6)(*[vda_checkpoint(_ptr(a), _ptr(b)) for a, b in pairs])
+    s = load().vda_backward_from_checkpoint(ctypes.byref(problem), arr, _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV),
+                                            _ptr(dG), _ptr(dK_txt), _ptr(dV_txt), _ptr(workspace), wb,
+                                            _stream(stream))
+    if check:
+        _check(s, "vda_backward_from_checkpoint")
     return s
 
 

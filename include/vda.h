@@ -314,6 +314,161 @@ typedef struct vda_merge_problem {
 vda_status vda_merge_project(const vda_merge_problem* p, const void* O_lin, const void* W_lin, const void* O_sm,
                              const void* W_sm, void* Y, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Token operators around the attention branches: layer norm, rotary
+ * positions, activation checkpoints in 8 bits.  Forward and backward are the
+ * exact derivatives of one another; statistics, sums and angles are float32
+ * or wider and an output is rounded once.
+ *
+ * They differ from the calls above in three ways.  (1) Tensors need only
+ * their element's alignment; pointers, widths and strides that are all
+ * multiples of 16 bytes take wider loads.  (2) They meet no device-side
+ * condition, so there is no error word and vda_sync_status does not apply to
+ * their workspace.  (3) Sizes may be zero: such a call checks its arguments,
+ * reads no tensor and returns VDA_OK (gradients of shared weights become 0).
+ * Every call is asynchronous on `stream`, allocates nothing, and may be
+ * captured into a CUDA graph.  Errors on the host, before anything is
+ * enqueued: VDA_ERR_INVALID_ARG (sizes, strides, unknown types, NULL or
+ * misaligned pointers), VDA_ERR_UNSUPPORTED (beyond the limits stated),
+ * VDA_ERR_WORKSPACE, VDA_ERR_CUDA (a launch).
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm over the last dimension.  Each token holds `heads` rows of D
+ * elements, each normalised by itself: heads = 1 and D the model width for the
+ * norm in front of a block, heads = H and D = d for the norm of every head of
+ * Q or K.  rows = tokens * heads.
+ *     m = sum(x) / D,  r = 1 / sqrt(sum((x - m)^2) / D + eps)
+ *     xh = (x - m) r,  y = xh * W + bias
+ * dtype: X, Y, dY, dX (float32 or bfloat16); w_dtype: W, bias.  dW and dbias
+ * are float32 (sums over all rows; the caller rounds them if it wants to).
+ * tokens in [0, 2^31), heads in [1, 65536], D in [1, 8192], eps finite, > 0.
+ * ld_x: elements from one token to the next in X and dX; ld_y: in Y and dY;
+ * 0 means heads * D, else at least that and below 2^31 (a slice of a wider
+ * tensor; the elements between the rows are neither read nor written). */
+typedef struct vda_norm_problem {
+  int64_t tokens;
+  int64_t ld_x, ld_y;
+  int32_t heads, D;
+  int32_t dtype, w_dtype; /* vda_dtype */
+  float eps;
+  int32_t reserved; /* 0 */
+} vda_norm_problem;
+
+/* Y from X.  W, bias: [D] or NULL (1 and 0).  mean, rstd: float32 [rows] or
+ * NULL; the backward needs them.  codes, scales (both or neither): the
+ * normalised rows xh as an 8-bit checkpoint (format below, rows of D; dense
+ * whatever ld_x), from which the backward can run instead of from X and mean.
+ * Y may be X where ld_x == ld_y; other overlaps are not allowed. */
+vda_status vda_layer_norm(const vda_norm_problem* p, const void* X, const void* W, const void* bias, void* Y,
+                          float* mean, float* rstd, void* codes, void* scales, void* stream);
+
+/* Y = xh * W + bias again, with xh from its checkpoint: the operand that the
+ * next product's weight gradient needs, which then need not be kept. */
+vda_status vda_layer_norm_from_checkpoint(const vda_norm_problem* p, const void* codes, const void* scales,
+                                          const void* W, const void* bias, void* Y, void* stream);
+
+/* Gradients of sum(dY * Y): with g = dY * W,
+ *     dX = r (g - mean(g) - xh mean(g xh)),
+ *     dW = sum over rows of dY xh,  dbias = sum over rows of dY
+ * written, not accumulated into.  W NULL: 1.  dW and dbias may each be NULL;
+ * with either given, `workspace` holds at least
+ * vda_layer_norm_backward_workspace_size() bytes (256-byte aligned; contents
+ * on entry do not matter; two calls that may overlap, or two graphs that may
+ * run at once, need one each).  The sums are added in an order that depends
+ * on the sizes alone, so equal calls give equal bits.  dX may be X, or dY
+ * where ld_x == ld_y; other overlaps are not allowed. */
+vda_status vda_layer_norm_backward_workspace_size(const vda_norm_problem* p, size_t* bytes);
+vda_status vda_layer_norm_backward(const vda_norm_problem* p, const void* dY, const void* X, const float* mean,
+                                   const float* rstd, const void* W, void* dX, float* dW, float* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with xh from its 8-bit checkpoint in place of X and mean. */
+vda_status vda_layer_norm_backward_from_checkpoint(const vda_norm_problem* p, const void* dY, const void* codes,
+                                                   const void* scales, const float* rstd, const void* W, void* dX,
+                                                   float* dW, float* dbias, void* workspace, size_t workspace_bytes,
+                                                   void* stream);
+
+/* Rotary positions over three axes (time, height, width) on Q and K.  The
+ * first d_t + d_y + d_x channels of a head turn in pairs, d_a / 2 of them by
+ * axis a (time's first, then height's, then width's): pair j of axis a turns by
+ * p_a theta^(-2 j / d_a),
+ *     (u, v) -> (u cos - v sin, u sin + v cos);
+ * the other channels are copied bit for bit.  pairing: VDA_ROPE_INTERLEAVED, a
+ * pair is two neighbouring channels; VDA_ROPE_HALVES, channels i and
+ * i + (d_t + d_y + d_x) / 2.
+ * Tokens: N = T * height * width per batch item, token (t, y, x) at
+ * (t * height + y) * width + x.  Positions: pos0[a] + step[a] * index on the
+ * axis (a later part of a long video starts at pos0[0]; step scales an axis),
+ * or, for packed sequences, `positions`, float32 [B, N, 3] on the device
+ * (pos0 and step are then not read; a position that is not finite gives NaN).
+ * Angles are formed in double: positions to 10^6 and beyond are as exact as
+ * near ones.  Q: H_q heads, K: H_k heads (either may be 0 with NULL
+ * pointers); dtype float32 or bfloat16.  layout VDA_LAYOUT_BTNHD:
+ * [B, N, H, d], where ld_q, ld_k (Q, K) and ld_qr, ld_kr (the turned ones) give
+ * the elements from one token to the next (0: H * d; else at least that and
+ * below 2^31; a batch item is N tokens).  VDA_LAYOUT_BHTND: [B, H, N, d],
+ * dense, the four strides 0.
+ * B, T, height, width >= 0, B * N < 2^31; H_q, H_k >= 0, H_q + H_k <= 65535; d
+ * in [1, 256]; d_t, d_y, d_x even, >= 0, their sum at most d; theta finite and
+ * > 0; pos0 and step finite. */
+typedef enum vda_rope_pairing { VDA_ROPE_INTERLEAVED = 0, VDA_ROPE_HALVES = 1 } vda_rope_pairing;
+typedef struct vda_rope_problem {
+  int64_t ld_q, ld_k, ld_qr, ld_kr;
+  double theta;
+  double pos0[3], step[3];
+  int32_t B, T, height, width;
+  int32_t H_q, H_k, d;
+  int32_t d_t, d_y, d_x;
+  int32_t dtype, layout, pairing;
+  int32_t reserved; /* 0 */
+} vda_rope_problem;
+
+/* Q, K -> Q_rot, K_rot.  An output may be its input where both have the same
+ * stride; other overlaps are not allowed. */
+vda_status vda_rope(const vda_rope_problem* p, const void* Q, const void* K, const float* positions, void* Q_rot,
+                    void* K_rot, void* stream);
+/* dQ_rot, dK_rot (strides ld_qr, ld_kr) -> dQ, dK (strides ld_q, ld_k): the
+ * turn the other way, which is also the exact inverse of vda_rope. */
+vda_status vda_rope_backward(const vda_rope_problem* p, const void* dQ_rot, const void* dK_rot,
+                             const float* positions, void* dQ, void* dK, void* stream);
+
+/* Activation checkpoints in 8 bits: a [rows, D] tensor (float32 or bfloat16)
+ * as e4m3 codes, uint8 [rows, D], and a scale byte per block of 32 neighbours
+ * of a row (the last block of a row may be short), uint8 [rows, ceil(D / 32)].
+ * With s the scale byte, an element stands for code * 2^(s - 127); s - 127 is
+ * the least integer e >= -127 with max|x| <= 448 * 2^e over the block's finite
+ * elements, and the code is x * 2^-e rounded to nearest even: off by at most
+ * 2^-4 |x|, or 2^-10 * 2^e where that is more.  (Magnitudes from 248 * 2^120 up
+ * take 240 * 2^120, so that unpacking stays finite.)  NaN and infinities are kept as
+ * NaN and leave the rest of their block alone.
+ * rows in [0, 2^40], D in [1, 2^24], rows * D < 2^46; ld: elements from one
+ * row of the tensor to the next (0: D; else at least D and below 2^31);
+ * codes and scales are dense. */
+typedef struct vda_checkpoint_problem {
+  int64_t rows, ld;
+  int32_t D;
+  int32_t dtype; /* vda_dtype of the tensor */
+} vda_checkpoint_problem;
+vda_status vda_checkpoint_pack(const vda_checkpoint_problem* p, const void* X, void* codes, void* scales,
+                               void* stream);
+vda_status vda_checkpoint_unpack(const vda_checkpoint_problem* p, const void* codes, const void* scales, void* X,
+                                 void* stream);
+
+/* vda_backward with Q, K, V, G, K_txt, V_txt as 8-bit checkpoints (each packed
+ * from its bfloat16 tensor as rows of D = 128, in the problem's layout): the
+ * gradients at the values that the checkpoints stand for.  `in`: six entries
+ * in that order (the last two are not read when n_txt == 0).  workspace: at
+ * least vda_backward_from_checkpoint_workspace_size() bytes, 256-byte aligned;
+ * the error word, the other arguments and errors as for vda_backward. */
+typedef struct vda_checkpoint {
+  const void* codes;
+  const void* scales;
+} vda_checkpoint;
+vda_status vda_backward_from_checkpoint_workspace_size(const vda_problem* p, size_t* bytes);
+vda_status vda_backward_from_checkpoint(const vda_problem* p, const vda_checkpoint* in, const void* dO, void* dQ,
+                                        void* dK, void* dV, void* dG, void* dK_txt, void* dV_txt, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of
  * `workspace`: VDA_OK, VDA_ERR_NOT_SPD or VDA_ERR_TIMEOUT (first one set),
  * or VDA_ERR_CUDA if the stream reports an error.  Blocking. */
