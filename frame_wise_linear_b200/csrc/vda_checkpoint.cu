@@ -33,10 +33,10 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* X, int64_t rows, int
     float x[VE];
 #pragma unroll
     for (int i = 0; i < VE; ++i) x[i] = q.get(i);
-    uint8_t c[VE];
+    Pack<uint8_t, VE> c;
     const int s = encode_block<VE>(x, c);
     if (in) {
-      store_codes<VE>(codes + row * D + (int64_t)v * VE, c);
+      c.store(codes + row * D + (int64_t)v * VE);
       if (v % (kBlock / VE) == 0) scales[row * nblk + v / (kBlock / VE)] = (uint8_t)s;
     }
   }
@@ -51,10 +51,10 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* codes, const
   for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = u / per_row;
     const int v = (int)(u - row * per_row);
-    CodePack<VE> c;
+    Pack<uint8_t, VE> c;
     float x[VE];
     c.load(codes + row * D + (int64_t)v * VE);
-    c.values(scale_of(scales[row * nblk + v / (kBlock / VE)]), x);
+    decode_pack<VE>(c, scale_of(scales[row * nblk + v / (kBlock / VE)]), x);
     Pack<T, VE> q;
 #pragma unroll
     for (int i = 0; i < VE; ++i) q.set(i, x[i]);

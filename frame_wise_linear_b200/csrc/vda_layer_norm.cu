@@ -6,20 +6,33 @@
 //   backward   g = dy w, dx = r (g - mean(g) - xh mean(g xh)),
 //              dw = sum over rows of dy xh, db = sum over rows of dy
 //
-// Both are bound by HBM: a row is read once, stays in registers between its
-// sums and its outputs, and is written once.  A row belongs to `tpr` threads,
-// each with 8 of its elements (one 16-byte vector of bf16, two of float32, or
-// 8 single elements where the row is not 16-byte aligned); up to 32 threads a
-// row is summed by shuffles, above that through shared memory.  The variance
-// is the mean of the squared differences from the mean that is already known
-// (two sums, no cancellation).  Everything is float32; an output is rounded
-// once.
+// Both are bound by HBM: a row is read once, stays on the SM between its sums
+// and its outputs, and is written once.  A row belongs to `tpr` threads, each
+// with 16 of its elements as 16-byte vectors (single elements where rows are
+// not 16-byte aligned).  A CTA walks over batches of rows, with the next batch
+// already on its way: every thread copies its own vectors into its own places
+// in shared memory (cp.async), so they need no barrier, cost no registers and
+// keep HBM busy while a batch is summed and written.  Several rows a batch
+// let the chains of their sums overlap, and share the barrier of a row's
+// warps.  Next to HBM the instructions count (a row of 4096 has 550 ns on its
+// SM in the backward), hence float32 in pairs.
+//
+// The row's sums: shuffles within a warp, and where a row has several warps
+// one exchange through shared memory with one barrier a batch.  In the forward
+// each thread takes the mean of its own elements first and the squares of the
+// differences from that; lanes and warps join (count, mean, squares):
+// sum of squares = sum_i M2_i + n_i (m_i - m)^2, exact algebra without the
+// cancellation of sum x^2 - D m^2, and no second pass over the row before m
+// is known.
 //
 // The gradients of w and b are sums over all rows.  A thread holds the same
 // columns of every row that its CTA takes, so it keeps their sums in
 // registers; each CTA writes one row of partial sums, and a second kernel
 // adds those rows in a fixed order (no atomics: the result does not depend on
-// the order in which CTAs run).
+// the order in which CTAs run).  Everything is float32; an output is rounded
+// once.
+#include <type_traits>
+
 #include "vda_internal.cuh"
 #include "vda_tokops.cuh"
 
@@ -27,9 +40,6 @@ namespace vda {
 namespace {
 
 using namespace tokops;
-
-constexpr int kPer = 8;   // elements of a row that one thread holds
-
 struct NormArgs {
   const void* X;       // forward: input; backward: input (or null: codes)
   const void* dY;      // backward
@@ -41,257 +51,462 @@ struct NormArgs {
   uint8_t* codes;      // forward: written (or null); backward: read (or null)
   uint8_t* scales;
   float* partial;      // backward: [gridDim.x][2 D] (dw then db), or null
-  int64_t tokens, ld_x, ld_y;   // ld_x: X (and dX); ld_y: Y, dY
+  int64_t rows, ld_x, ld_y;   // ld_x: X (and dX); ld_y: Y, dY; from one token to the next
+  uint64_t by_heads;   // ceil(2^64 / heads), or 0: every row is a token
   int heads, D, tpr;
   float eps, inv_d;
   int w_bf16;
 };
 
+// Element offset of a row: token row / heads, head row % heads.  The quotient
+// by multiplication is exact: row * heads < 2^64.
+__device__ __forceinline__ int64_t row_at(const NormArgs& a, int64_t row, int64_t ld) {
+  if (a.by_heads == 0) return row * ld;
+  const int64_t tok = (int64_t)__umul64hi((uint64_t)row, a.by_heads);
+  return tok * ld + (row - tok * a.heads) * a.D;
+}
+
 __device__ __forceinline__ float load_w(const void* w, int i, int w_bf16) {
   return w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
 }
-
-// A row's place: token and head, advanced by a fixed number of rows.
-struct RowPos {
-  int64_t row, tok;
-  int head;
-  __device__ __forceinline__ RowPos(int64_t r, int heads) : row(r) {
-    if (heads == 1) {
-      tok = r;
-      head = 0;
-    } else {
-      tok = r / heads;
-      head = (int)(r - tok * heads);
-    }
+// Sums over a group of neighbouring lanes (lanes: a power of two).
+template <int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
   }
-  __device__ __forceinline__ void advance(int64_t by, int64_t dtok, int dhead, int heads) {
-    row += by;
-    tok += dtok;
-    head += dhead;
-    if (head >= heads) {
-      head -= heads;
-      ++tok;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+constexpr int kThreads = 256;   // of a CTA at most, and the ring's stride
+
+// What a thread is in its CTA, and which columns it holds: vectors t + k tpr,
+// k < NV, of VE elements; kFull: every thread has all of them.
+template <int VE, int NV, bool kFull>
+struct Place {
+  int t, group, groups, tpr, nvec, lanes, warps, lane, warp, first;
+  __device__ __forceinline__ explicit Place(const NormArgs& a) {
+    tpr = a.tpr;
+    t = (int)threadIdx.x % a.tpr;
+    group = (int)threadIdx.x / a.tpr;
+    groups = (int)blockDim.x / a.tpr;
+    nvec = a.D / VE;
+    lanes = a.tpr < 32 ? a.tpr : 32;
+    warps = a.tpr < 32 ? 1 : a.tpr >> 5;
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    first = warp / warps * warps;   // the row's first warp
+  }
+  __device__ __forceinline__ int vec(int k) const { return t + k * tpr; }
+  __device__ __forceinline__ bool has(int k) const { return kFull || vec(k) < nvec; }
+  __device__ __forceinline__ int elements() const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) n += has(k) ? VE : 0;
+    return n;
+  }
+  // Elements that warp i of a row holds: vectors 32 i + k tpr .. + 31.
+  __device__ __forceinline__ int warp_elements(int i) const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int left = nvec - (i * 32 + k * tpr);
+      n += left < 0 ? 0 : (left > 32 ? 32 : left);
     }
+    return n * VE;
   }
 };
 
-// Sums of v over the threads of a row; every thread gets them.  Rows of up to
-// 32 threads: shuffles.  Above: the row's warps leave their sums in one half
-// of `red` (the halves alternate from call to call, so one barrier a call is
-// enough), and every thread adds them in the same order.
-struct RowSum {
-  float2* red;   // [2][32]
-  int tpr, warps, first, half;
-  __device__ __forceinline__ RowSum(float2* r, int t) : red(r), tpr(t), half(0) {
-    warps = t >> 5;
-    first = warps ? ((int)threadIdx.x / t) * warps : 0;
-  }
-  __device__ __forceinline__ float2 operator()(float2 v) {
-    for (int o = (tpr < 32 ? tpr : 32) / 2; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if (tpr <= 32) return v;
-    float2* r = red + half * 32;
-    half ^= 1;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = r[first];
-    for (int i = 1; i < warps; ++i) {
-      const float2 o = r[first + i];
-      v.x += o.x;
-      v.y += o.y;
-    }
-    return v;
-  }
+// A thread's elements of a row as pairs: element e = k VE + i is half e % 2 of
+// pair e / 2.
+template <int N>
+struct Pairs {
+  float2 p[N / 2];
+  __device__ __forceinline__ void set(int e, float v) { (e % 2 ? p[e / 2].y : p[e / 2].x) = v; }
+  __device__ __forceinline__ float get(int e) const { return e % 2 ? p[e / 2].y : p[e / 2].x; }
 };
 
-// Vectors of VE elements, NV = kPer / VE a thread: vector k of thread t of a
-// row is number t + k tpr.
-template <typename T, int VE>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
-  constexpr int NV = kPer / VE;
-  __shared__ float2 red[64];
-  const int t = (int)threadIdx.x % a.tpr, group = (int)threadIdx.x / a.tpr;
-  const int groups = (int)blockDim.x / a.tpr;
-  const int nvec = a.D / VE, nblk = (a.D + kBlock - 1) / kBlock;
-  float w[kPer], b[kPer];
+template <int VE, int NV, bool kFull>
+__device__ __forceinline__ void load_columns(const void* w, const NormArgs& a, const Place<VE, NV, kFull>& p,
+                                             float none, Pairs<NV * VE>& out) {
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const int v = t + k * a.tpr, c = v * VE + i;
-      w[k * VE + i] = a.W && v < nvec ? load_w(a.W, c, a.w_bf16) : 1.f;
-      b[k * VE + i] = a.bias && v < nvec ? load_w(a.bias, c, a.w_bf16) : 0.f;
+    for (int i = 0; i < VE; ++i)
+      out.set(k * VE + i, w && p.has(k) ? load_w(w, p.vec(k) * VE + i, a.w_bf16) : none);
+}
+
+// Where the threads of a CTA find the elements of a batch: kRows rows of every
+// row group, two batches on the SM, one being worked on and one on its way.
+// kAsync: in shared memory, [2][kRows][NV][kThreads] vectors from `base`, each
+// thread's own, filled by its own cp.async (so no barrier is needed to read
+// them).  Else (bf16 or codes that are not aligned, which cp.async cannot
+// fetch one by one) straight from global memory, the second time from the
+// caches.
+template <typename T, int VE, int NV, int kRows, bool kAsync>
+struct Batch {
+  static constexpr int kBytes = kAsync ? 2 * kRows * NV * VE * (int)sizeof(T) * kThreads : 0;
+  T* place;
+  __device__ __forceinline__ explicit Batch(void* base) { place = static_cast<T*>(base) + (int)threadIdx.x * VE; }
+  __device__ __forceinline__ T* slot(int buf, int r, int k) const {
+    return place + buf * (kRows * NV * kThreads * VE) + (r * NV + k) * (kThreads * VE);
+  }
+  template <bool kFull>
+  __device__ __forceinline__ void fetch(int buf, int r, const T* row, const Place<VE, NV, kFull>& p) const {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (p.has(k)) async_copy<VE * (int)sizeof(T)>(slot(buf, r, k), row + p.vec(k) * VE);
     }
-  RowSum sum(red, a.tpr);
-  const int64_t rows = a.tokens * a.heads, by = (int64_t)gridDim.x * groups;
-  const int64_t dtok = by / a.heads;
-  const int dhead = (int)(by - dtok * a.heads);
-  RowPos p((int64_t)blockIdx.x * groups + group, a.heads);
-  // Every thread of the block makes the same number of trips: the sums and
-  // the block maxima need them all.
-  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < rows; r0 += by) {
-    const bool live = p.row < rows;
-    const T* xr = static_cast<const T*>(a.X) + p.tok * a.ld_x + (int64_t)p.head * a.D;
-    float x[kPer];
-    float2 s = make_float2(0.f, 0.f);
+  }
+  template <bool kFull>
+  __device__ __forceinline__ Pack<T, VE> get(int buf, int r, int k, const T* row, const Place<VE, NV, kFull>& p) const {
+    Pack<T, VE> q;
+    if constexpr (!kFull) q.zero();
+    if (p.has(k)) q.load(kAsync ? slot(buf, r, k) : row + p.vec(k) * VE);
+    return q;
+  }
+  // All of the thread's elements of a row, zeros where it has none.
+  template <bool kFull>
+  __device__ __forceinline__ void get(int buf, int r, const T* row, const Place<VE, NV, kFull>& p,
+                                      Pairs<NV * VE>& out) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = t + k * a.tpr;
-      Pack<T, VE> q;
-      if (live && v < nvec) q.load(xr + (int64_t)v * VE);
-      else q.zero();
+      const Pack<T, VE> q = get(buf, r, k, row, p);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        x[k * VE + i] = q.get(i);
-        s.x += x[k * VE + i];
-      }
+      for (int i = 0; i < VE; ++i) out.set(k * VE + i, q.get(i));
     }
-    const float mean = sum(s).x * a.inv_d;
-    s.x = 0.f;
+  }
+};
+
+// CTAs of an SM that the kernels are compiled for, by the elements a thread
+// holds (two: up to 128 registers a thread; with three the rows of a batch
+// spill: 45360 x 4096 bf16 forward 190 us against 148, backward 234 against
+// 205).
+constexpr int ctas_of(int per) { return per == 32 ? 1 : 2; }
+
+template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull>
+__global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(const NormArgs a) {
+  constexpr int N = NV * VE;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][kRows][kThreads / 32];   // (mean, squares) of each warp's part of a row
+  const Place<VE, NV, kFull> p(a);
+  const int nblk = (a.D + kBlock - 1) / kBlock;
+  const Batch<T, VE, NV, kRows, kAsync> in(ring);
+  const T* X = static_cast<const T*>(a.X);
+  // Row r of a batch that starts at row0: row0 + r groups + group.
+  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  auto fetch = [&](int buf, int64_t row0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row < a.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
+    }
+  };
+  int64_t row0 = blockIdx.x * span;
+  fetch(0, row0);
+  async_commit();
+  Pairs<N> w, b;
+  load_columns(a.W, a, p, 1.f, w);
+  load_columns(a.bias, a, p, 0.f, b);
+  const int n_t = p.elements();
+  const float count_t = (float)n_t, inv_t = 1.f / (float)(n_t > 1 ? n_t : 1);
+  const float inv_w = p.warps > 1 ? 1.f / (float)p.warp_elements(p.warp - p.first) : a.inv_d;
+  // In the exchange lanes 0 - 15 and 16 - 31 look at one warp each of two rows.
+  const int peer = p.lane & 15;
+  const bool in_row = peer < p.warps;
+  const float weight = in_row ? (float)p.warp_elements(peer) * a.inv_d : 0.f;
+  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+    fetch(buf ^ 1, row0 + step);
+    async_commit();
+    async_wait<1>();
+    float mean[kRows], rstd[kRows], s[kRows], m2[kRows], own[kRows];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const bool in = t + k * a.tpr < nvec;
-        x[k * VE + i] = in ? x[k * VE + i] - mean : 0.f;
-        s.x += x[k * VE + i] * x[k * VE + i];
-      }
-    const float rstd = 1.f / sqrtf(sum(s).x * a.inv_d + a.eps);
-    T* yr = static_cast<T*>(a.Y) + p.tok * a.ld_y + (int64_t)p.head * a.D;
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      s[r] = m2[r] = own[r] = 0.f;
+      if (row < a.rows) {
+        Pairs<N> x;
+        in.get(buf, r, X + row_at(a, row, a.ld_x), p, x);
+        float2 sum = x.p[0];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = t + k * a.tpr;
-      const bool in = live && v < nvec;
-      Pack<T, VE> q;
-      float xh[VE];
+        for (int j = 1; j < N / 2; ++j) sum = add2(sum, x.p[j]);
+        s[r] = sum.x + sum.y;
+        own[r] = s[r] * inv_t;   // the thread's own mean
+        float2 sq = both(0.f);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        xh[i] = x[k * VE + i] * rstd;
-        q.set(i, xh[i] * w[k * VE + i] + b[k * VE + i]);
-      }
-      if (in) q.store(yr + (int64_t)v * VE);
-      if (a.codes) {
-        // A thread without this vector adds nothing to the block's maximum.
-        if (!in) {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) xh[i] = 0.f;
+        for (int j = 0; j < N / 2; ++j) {
+          float2 d = add2(x.p[j], both(-own[r]));
+          if constexpr (!kFull) {
+            if (!p.has(2 * j / VE)) d.x = 0.f;
+            if (!p.has((2 * j + 1) / VE)) d.y = 0.f;
+          }
+          sq = fma2(d, d, sq);
         }
-        uint8_t c[VE];
-        const int sb = encode_block<VE>(xh, c);
-        if (in) {
-          store_codes<VE>(a.codes + p.row * a.D + (int64_t)v * VE, c);
-          if (v % (kBlock / VE) == 0) a.scales[p.row * nblk + v / (kBlock / VE)] = (uint8_t)sb;
-        }
+        m2[r] = sq.x + sq.y;
       }
     }
-    if (live && t == 0) {
-      if (a.mean) a.mean[p.row] = mean;
-      if (a.rstd) a.rstd[p.row] = rstd;
+    lanes_sum(s, p.lanes);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      mean[r] = s[r] * inv_w;
+      const float d = own[r] - mean[r];
+      m2[r] += kFull || n_t > 0 ? count_t * d * d : 0.f;
     }
-    p.advance(by, dtok, dhead, a.heads);
+    lanes_sum(m2, p.lanes);
+    if (p.warps > 1) {
+      if (p.lane == 0) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) red[buf][r][p.warp] = make_float2(mean[r], m2[r]);
+      }
+      // A warp that writes this half again has passed the barrier of the batch
+      // between, as has every reader after reading.
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRows; r += 2) {
+        const int at = kRows > 1 ? r + (p.lane >> 4) : 0;
+        const float2 e = in_row ? red[buf][at][p.first + peer] : make_float2(0.f, 0.f);
+        const float m = half_warp_sum(e.x * weight);
+        const float d = e.x - m;
+        const float var = half_warp_sum(in_row ? e.y * a.inv_d + weight * d * d : 0.f);
+        const float rs = 1.f / sqrtf(var + a.eps);
+        mean[r] = __shfl_sync(0xffffffffu, m, 0);
+        rstd[r] = __shfl_sync(0xffffffffu, rs, 0);
+        if (kRows > 1) {
+          mean[r + 1 < kRows ? r + 1 : r] = __shfl_sync(0xffffffffu, m, 16);
+          rstd[r + 1 < kRows ? r + 1 : r] = __shfl_sync(0xffffffffu, rs, 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) rstd[r] = 1.f / sqrtf(m2[r] * a.inv_d + a.eps);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row >= a.rows) break;
+      const T* xr = X + row_at(a, row, a.ld_x);
+      T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
+      Pairs<N> x, y;
+      in.get(buf, r, xr, p, x);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        x.p[j] = mul2(add2(x.p[j], both(-mean[r])), both(rstd[r]));
+        y.p[j] = fma2(x.p[j], w.p[j], b.p[j]);
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        Pack<T, VE> q;
+        if constexpr (VE > 1) {
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) q.set2(i, y.p[(k * VE + i) / 2]);
+        } else {
+          q.set(0, y.get(k));
+        }
+        if (p.has(k)) q.store(yr + p.vec(k) * VE);
+        if (a.codes) {
+          // A thread without this vector adds nothing to the block's maximum.
+          float xh[VE];
+#pragma unroll
+          for (int i = 0; i < VE; ++i) xh[i] = p.has(k) ? x.get(k * VE + i) : 0.f;
+          Pack<uint8_t, VE> c;
+          const int sb = encode_block<VE>(xh, c);
+          if (p.has(k)) {
+            c.store(a.codes + row * a.D + p.vec(k) * VE);
+            if (p.vec(k) % (kBlock / VE) == 0) a.scales[row * nblk + p.vec(k) / (kBlock / VE)] = (uint8_t)sb;
+          }
+        }
+      }
+      if (p.t == 0) {
+        if (a.mean) a.mean[row] = mean[r];
+        if (a.rstd) a.rstd[row] = rstd[r];
+      }
+    }
+  }
+}
+
+// The scale bytes of a thread's vectors of a row.
+template <int VE, int NV, bool kFull>
+__device__ __forceinline__ void load_scales(const NormArgs& a, int64_t row, int nblk, const Place<VE, NV, kFull>& p,
+                                            int (&sb)[NV]) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (p.has(k)) sb[k] = a.scales[row * nblk + p.vec(k) / (kBlock / VE)];
+}
+
+// All of a thread's elements of a row of codes, scaled.
+template <int VE, int NV, int kRows, bool kAsync, bool kFull>
+__device__ __forceinline__ void get_codes(const Batch<uint8_t, VE, NV, kRows, kAsync>& in, int buf, int r,
+                                          const uint8_t* row, const Place<VE, NV, kFull>& p, const int (&sb)[NV],
+                                          Pairs<NV * VE>& out) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    float x[VE];
+    decode_pack<VE>(in.get(buf, r, k, row, p), scale_of(sb[k]), x);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) out.set(k * VE + i, x[i]);
   }
 }
 
 // The backward: X with mean and rstd, or (kCodes) the 8-bit normalised row
 // with rstd.  Writes dX, and with a.partial the CTA's sums of dy xh and dy.
-template <typename T, int VE, bool kCodes>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
-  constexpr int NV = kPer / VE;
-  extern __shared__ float fold[];   // groups > 1: [groups][2 D]
-  __shared__ float2 red[64];
-  const int t = (int)threadIdx.x % a.tpr, group = (int)threadIdx.x / a.tpr;
-  const int groups = (int)blockDim.x / a.tpr;
-  const int nvec = a.D / VE, nblk = (a.D + kBlock - 1) / kBlock;
-  float w[kPer], dw[kPer], db[kPer];
+// A batch's elements are read twice from shared memory, for the sums and for
+// dX: kept in registers they would cost 32 a row, and the occupancy with them.
+template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull, bool kCodes>
+__global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(const NormArgs a) {
+  constexpr int N = NV * VE, kSb = kCodes ? NV : 1;
+  using U = typename std::conditional<kCodes, uint8_t, T>::type;   // what xh comes from
+  using InY = Batch<T, VE, NV, kRows, kAsync>;
+  using InX = Batch<U, VE, NV, kRows, kAsync>;
+  extern __shared__ __align__(16) uint8_t ring[];   // afterwards: groups > 1: [groups][2 D] partial sums
+  __shared__ float red[2][2 * kRows][kThreads / 32];
+  const Place<VE, NV, kFull> p(a);
+  const int nblk = (a.D + kBlock - 1) / kBlock;
+  const InY iny(ring);
+  const InX inx(ring + InY::kBytes);
+  const T* dY = static_cast<const T*>(a.dY);
+  const U* X = kCodes ? reinterpret_cast<const U*>(a.codes) : static_cast<const U*>(a.X);
+  auto x_at = [&](int64_t row) { return kCodes ? row * a.D : row_at(a, row, a.ld_x); };
+  // rstd, and mean or the scale bytes, of the batch that is worked on and of
+  // the next: loaded with it, so that they too are there when it is.
+  float mean[kRows], rstd[kRows], next_mean[kRows], next_rstd[kRows];
+  int sb[kRows][kSb], next_sb[kRows][kSb];
+  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  auto fetch = [&](int buf, int64_t row0) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const int v = t + k * a.tpr;
-      w[k * VE + i] = a.W && v < nvec ? load_w(a.W, v * VE + i, a.w_bf16) : 1.f;
-      dw[k * VE + i] = db[k * VE + i] = 0.f;
-    }
-  RowSum sum(red, a.tpr);
-  const int64_t rows = a.tokens * a.heads, by = (int64_t)gridDim.x * groups;
-  const int64_t dtok = by / a.heads;
-  const int dhead = (int)(by - dtok * a.heads);
-  RowPos p((int64_t)blockIdx.x * groups + group, a.heads);
-  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < rows; r0 += by) {
-    const bool live = p.row < rows;
-    const int64_t at_x = p.tok * a.ld_x + (int64_t)p.head * a.D, at_y = p.tok * a.ld_y + (int64_t)p.head * a.D;
-    const float mean = !kCodes && live ? a.mean[p.row] : 0.f, rstd = live ? a.rstd[p.row] : 0.f;
-    float g[kPer], xh[kPer];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = t + k * a.tpr;
-      const bool in = live && v < nvec;
-      Pack<T, VE> q;
-      if (in) q.load(static_cast<const T*>(a.dY) + at_y + (int64_t)v * VE);
-      else q.zero();
-      float x[VE];
-      if constexpr (kCodes) {
-        CodePack<VE> c;
-        float sc = 0.f;
-        if (in) {
-          c.load(a.codes + p.row * a.D + (int64_t)v * VE);
-          sc = scale_of(a.scales[p.row * nblk + v / (kBlock / VE)]);
-          c.values(sc, x);
-        }
-      } else {
-        Pack<T, VE> u;
-        if (in) {
-          u.load(static_cast<const T*>(a.X) + at_x + (int64_t)v * VE);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) x[i] = (u.get(i) - mean) * rstd;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const int e = k * VE + i;
-        const float dy = q.get(i);
-        xh[e] = in ? x[i] : 0.f;
-        g[e] = dy * w[e];
-        dw[e] += dy * xh[e];
-        db[e] += dy;
-        s.x += g[e];
-        s.y += g[e] * xh[e];
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row < a.rows) {
+        iny.fetch(buf, r, dY + row_at(a, row, a.ld_y), p);
+        inx.fetch(buf, r, X + x_at(row), p);
+        next_rstd[r] = a.rstd[row];
+        if constexpr (kCodes) load_scales(a, row, nblk, p, next_sb[r]);
+        else next_mean[r] = a.mean[row];
       }
     }
-    s = sum(s);
-    s.x *= a.inv_d;
-    s.y *= a.inv_d;
+  };
+  // The thread's dy, and xh, of row r.
+  auto get = [&](int buf, int r, int64_t row, Pairs<N>& dy, Pairs<N>& xh) {
+    iny.get(buf, r, dY + row_at(a, row, a.ld_y), p, dy);
+    if constexpr (kCodes) {
+      get_codes(inx, buf, r, X + x_at(row), p, sb[r], xh);
+    } else {
+      inx.get(buf, r, X + x_at(row), p, xh);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = t + k * a.tpr;
-      Pack<T, VE> q;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) q.set(i, rstd * (g[k * VE + i] - s.x - xh[k * VE + i] * s.y));
-      if (live && v < nvec) q.store(static_cast<T*>(a.Y) + at_x + (int64_t)v * VE);
+      for (int j = 0; j < N / 2; ++j) xh.p[j] = mul2(add2(xh.p[j], both(-mean[r])), both(rstd[r]));
     }
-    p.advance(by, dtok, dhead, a.heads);
+  };
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    next_mean[r] = next_rstd[r] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSb; ++k) next_sb[r][k] = 0;
+  }
+  int64_t row0 = blockIdx.x * span;
+  fetch(0, row0);
+  async_commit();
+  Pairs<N> w, dw, db;
+  load_columns(a.W, a, p, 1.f, w);
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) dw.p[j] = db.p[j] = both(0.f);
+  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      mean[r] = next_mean[r];
+      rstd[r] = next_rstd[r];
+#pragma unroll
+      for (int k = 0; k < kSb; ++k) sb[r][k] = next_sb[r][k];
+    }
+    fetch(buf ^ 1, row0 + step);
+    async_commit();
+    async_wait<1>();
+    float s[2 * kRows];   // of g, then of g xh
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      float2 s1 = both(0.f), s2 = both(0.f);
+      if (row < a.rows) {
+        Pairs<N> dy, xh;
+        get(buf, r, row, dy, xh);
+        // Where the thread has no vector dy is 0: nothing is added.
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 t = mul2(dy.p[j], xh.p[j]);
+          dw.p[j] = add2(dw.p[j], t);
+          db.p[j] = add2(db.p[j], dy.p[j]);
+          s1 = fma2(dy.p[j], w.p[j], s1);
+          s2 = fma2(t, w.p[j], s2);
+        }
+      }
+      s[r] = s1.x + s1.y;
+      s[kRows + r] = s2.x + s2.y;
+    }
+    lanes_sum(s, p.lanes);
+    if (p.warps > 1) {
+      if (p.lane == 0) {
+#pragma unroll
+        for (int n = 0; n < 2 * kRows; ++n) red[buf][n][p.warp] = s[n];
+      }
+      __syncthreads();   // the halves alternate: see the forward
+#pragma unroll
+      for (int n = 0; n < 2 * kRows; n += 2) {
+        const int peer = p.lane & 15;
+        const float sum = half_warp_sum(peer < p.warps ? red[buf][n + (p.lane >> 4)][p.first + peer] : 0.f);
+        s[n] = __shfl_sync(0xffffffffu, sum, 0);
+        s[n + 1] = __shfl_sync(0xffffffffu, sum, 16);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row >= a.rows) break;
+      T* dx = static_cast<T*>(a.Y) + row_at(a, row, a.ld_x);
+      const float2 c1 = both(-s[r] * a.inv_d), c2 = both(-s[kRows + r] * a.inv_d), rs = both(rstd[r]);
+      Pairs<N> dy, xh;
+      get(buf, r, row, dy, xh);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) xh.p[j] = mul2(rs, fma2(dy.p[j], w.p[j], fma2(xh.p[j], c2, c1)));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        Pack<T, VE> d;
+        if constexpr (VE > 1) {
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) d.set2(i, xh.p[(k * VE + i) / 2]);
+        } else {
+          d.set(0, xh.get(k));
+        }
+        if (p.has(k)) d.store(dx + p.vec(k) * VE);
+      }
+    }
   }
   if (!a.partial) return;
   float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
-  if (groups > 1) out = fold + (int64_t)group * 2 * a.D;
+  float* fold = reinterpret_cast<float*>(ring);
+  if (p.groups > 1) {
+    async_wait<0>();
+    __syncthreads();   // every thread has read its last rows
+    out = fold + p.group * 2 * a.D;
+  }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int v = t + k * a.tpr;
-    if (v < nvec) {
+    if (p.has(k)) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        out[v * VE + i] = dw[k * VE + i];
-        out[a.D + v * VE + i] = db[k * VE + i];
+        out[p.vec(k) * VE + i] = dw.get(k * VE + i);
+        out[a.D + p.vec(k) * VE + i] = db.get(k * VE + i);
       }
     }
   }
-  if (groups > 1) {
+  if (p.groups > 1) {
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.D; c += blockDim.x) {
       float v = 0.f;
-      for (int q = 0; q < groups; ++q) v += fold[q * 2 * a.D + c];
+      for (int q = 0; q < p.groups; ++q) v += fold[q * 2 * a.D + c];
       a.partial[(int64_t)blockIdx.x * 2 * a.D + c] = v;
     }
   }
@@ -318,120 +533,194 @@ __global__ void __launch_bounds__(256) norm_fold_kernel(const float* partial, in
 }
 
 // y = xh w + b from the 8-bit normalised rows.
-template <typename T, int VE>
-__global__ void __launch_bounds__(1024) norm_apply_kernel(const NormArgs a) {
-  constexpr int NV = kPer / VE;
-  const int t = (int)threadIdx.x % a.tpr, group = (int)threadIdx.x / a.tpr;
-  const int groups = (int)blockDim.x / a.tpr;
-  const int nvec = a.D / VE, nblk = (a.D + kBlock - 1) / kBlock;
-  float w[kPer], b[kPer];
+template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull>
+__global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_apply_kernel(const NormArgs a) {
+  constexpr int N = NV * VE;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Place<VE, NV, kFull> p(a);
+  const int nblk = (a.D + kBlock - 1) / kBlock;
+  const Batch<uint8_t, VE, NV, kRows, kAsync> in(ring);
+  int sb[kRows][NV], next_sb[kRows][NV] = {};
+  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  auto fetch = [&](int buf, int64_t row0) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const int v = t + k * a.tpr, c = v * VE + i;
-      w[k * VE + i] = a.W && v < nvec ? load_w(a.W, c, a.w_bf16) : 1.f;
-      b[k * VE + i] = a.bias && v < nvec ? load_w(a.bias, c, a.w_bf16) : 0.f;
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row < a.rows) {
+        in.fetch(buf, r, a.codes + row * a.D, p);
+        load_scales(a, row, nblk, p, next_sb[r]);
+      }
     }
-  const int64_t rows = a.tokens * a.heads, by = (int64_t)gridDim.x * groups;
-  const int64_t dtok = by / a.heads;
-  const int dhead = (int)(by - dtok * a.heads);
-  RowPos p((int64_t)blockIdx.x * groups + group, a.heads);
-  for (; p.row < rows; p.advance(by, dtok, dhead, a.heads)) {
-    T* yr = static_cast<T*>(a.Y) + p.tok * a.ld_y + (int64_t)p.head * a.D;
+  };
+  int64_t row0 = blockIdx.x * span;
+  fetch(0, row0);
+  async_commit();
+  Pairs<N> w, b;
+  load_columns(a.W, a, p, 1.f, w);
+  load_columns(a.bias, a, p, 0.f, b);
+  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = t + k * a.tpr;
-      if (v >= nvec) continue;
-      CodePack<VE> c;
-      float x[VE];
-      c.load(a.codes + p.row * a.D + (int64_t)v * VE);
-      c.values(scale_of(a.scales[p.row * nblk + v / (kBlock / VE)]), x);
-      Pack<T, VE> q;
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int i = 0; i < VE; ++i) q.set(i, x[i] * w[k * VE + i] + b[k * VE + i]);
-      q.store(yr + (int64_t)v * VE);
+      for (int k = 0; k < NV; ++k) sb[r][k] = next_sb[r][k];
+    fetch(buf ^ 1, row0 + step);
+    async_commit();
+    async_wait<1>();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * p.groups + p.group;
+      if (row >= a.rows) break;
+      T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
+      Pairs<N> x;
+      get_codes(in, buf, r, a.codes + row * a.D, p, sb[r], x);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) x.p[j] = fma2(x.p[j], w.p[j], b.p[j]);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        Pack<T, VE> q;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) q.set(i, x.get(k * VE + i));
+        if (p.has(k)) q.store(yr + p.vec(k) * VE);
+      }
     }
   }
 }
 
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Threads of a row and of a block, and rows of a block.  A row takes as many
-// threads as it has groups of 8 elements: a power of two up to 32 (at least
-// the lanes of one 32-element block of codes), or whole warps.
+// Threads of a row and of a CTA, and rows of a CTA.  A thread holds 16
+// elements of a row (8 where a row would not fill the lanes of a block of
+// codes with 16, 32 where a row would need more than 256 threads); a row
+// takes a power of two up to 32 threads, at least the lanes of one block, or
+// whole warps.
 struct Shape {
-  int tpr, threads, groups;
+  int per, tpr, threads, groups;
+  bool full;
 };
 Shape shape_for(int D, int ve) {
-  const int need = ((D + ve - 1) / ve + kPer / ve - 1) / (kPer / ve);
-  int tpr = kBlock / ve;
+  const int least = kBlock / ve, nvec = D / ve;
+  const int per = D <= 8 * least ? 8 : (D <= 16 * kThreads ? 16 : 32);
+  const int need = (nvec + per / ve - 1) / (per / ve);
+  int tpr = least;
   while (tpr < 32 && tpr < need) tpr *= 2;
   if (need > 32) tpr = (need + 31) / 32 * 32;
-  const int groups = tpr >= 256 ? 1 : 256 / tpr;
-  return Shape{tpr, tpr * groups, groups};
+  const int groups = kThreads / tpr;
+  return Shape{per, tpr, tpr * groups, groups, nvec == tpr * (per / ve)};
 }
 
-// CTAs for `rows` rows: enough for every SM to hold 2048 threads' worth, or
-// fewer where there are fewer rows.
-int grid_for(int64_t rows, const Shape& s) {
-  const int64_t blocks = (rows + s.groups - 1) / s.groups;
-  const int64_t most = 148 * (s.threads > 1024 ? 1 : 1024 / s.threads);
-  return (int)(blocks < most ? blocks : most);
+// CTAs for `rows` rows in batches of `n` rows a group: as many as are resident
+// at once, or as there are batches.
+int grid_for(int64_t rows, const Shape& s, int n) {
+  const int64_t batches = (rows + (int64_t)s.groups * n - 1) / ((int64_t)s.groups * n);
+  const int64_t most = 148 * ctas_of(s.per);
+  return (int)(batches < most ? batches : most);
+}
+// Batches of several rows where every CTA gets one all the same.
+bool batched(int64_t rows, const Shape& s, int n) {
+  return rows >= (int64_t)grid_for(rows, s, 1) * s.groups * n;
 }
 
 // 16-byte vectors where the width, the strides and the pointers allow them.
 template <typename T>
 bool wide(const NormArgs& a) {
   const int ve = 16 / (int)sizeof(T);
-  const bool c = !a.codes || (aligned_to(a.codes, ve) && a.D % ve == 0);
-  return c && a.D % ve == 0 && a.ld_x % ve == 0 && a.ld_y % ve == 0 && aligned_to(a.X, 16) && aligned_to(a.dY, 16) &&
-         aligned_to(a.Y, 16);
+  return a.D % ve == 0 && a.ld_x % ve == 0 && a.ld_y % ve == 0 && aligned_to(a.X, 16) && aligned_to(a.dY, 16) &&
+         aligned_to(a.Y, 16) && aligned_to(a.codes, ve);
 }
 
-template <typename T, int VE>
-cudaError_t fwd(NormArgs a, cudaStream_t st) {
-  const Shape s = shape_for(a.D, VE);
-  a.tpr = s.tpr;
-  norm_fwd_kernel<T, VE><<<grid_for(a.tokens * a.heads, s), s.threads, 0, st>>>(a);
+template <typename Kernel>
+cudaError_t launch(Kernel k, int grid, int threads, int sh, const NormArgs& a, cudaStream_t st) {
+  if (sh > 46 * 1024) {   // with the static part, what a launch may have without asking is 48 KB
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sh);
+    if (e != cudaSuccess) return e;
+  }
+  k<<<grid, threads, sh, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int VE>
-cudaError_t bwd(NormArgs a, float* dW, float* db, cudaStream_t st) {
-  const Shape s = shape_for(a.D, VE);
+enum Pass { kForward, kBackward, kApply };
+
+template <typename T, int VE, int NV, int kRows, bool kFull>
+cudaError_t run_rows(Pass pass, const NormArgs& a, const Shape& s, cudaStream_t st) {
+  constexpr bool kX = VE * sizeof(T) >= 4, kC = VE >= 4, kBoth = kX && kC;   // what cp.async can fetch
+  const int grid = grid_for(a.rows, s, kRows);
+  if (pass == kForward)
+    return launch(norm_fwd_kernel<T, VE, NV, kRows, kX, kFull>, grid, s.threads, Batch<T, VE, NV, kRows, kX>::kBytes, a,
+                  st);
+  if (pass == kApply)
+    return launch(norm_apply_kernel<T, VE, NV, kRows, kC, kFull>, grid, s.threads,
+                  Batch<uint8_t, VE, NV, kRows, kC>::kBytes, a, st);
+  const int fold = a.partial && s.groups > 1 ? s.groups * 2 * a.D * (int)sizeof(float) : 0;
+  if (a.codes) {
+    const int sh = Batch<T, VE, NV, kRows, kBoth>::kBytes + Batch<uint8_t, VE, NV, kRows, kBoth>::kBytes;
+    return launch(norm_bwd_kernel<T, VE, NV, kRows, kBoth, kFull, true>, grid, s.threads, sh > fold ? sh : fold, a, st);
+  }
+  const int sh = 2 * Batch<T, VE, NV, kRows, kX>::kBytes;
+  return launch(norm_bwd_kernel<T, VE, NV, kRows, kX, kFull, false>, grid, s.threads, sh > fold ? sh : fold, a, st);
+}
+
+// Rows of a batch: 128 bytes of a thread's loads on their way, where there are
+// rows enough.
+constexpr int batch_rows(int element, int per, bool backward) {
+  const int n = 128 / (per * element) / (backward ? 2 : 1);
+  return n < 1 ? 1 : n > 4 ? 4 : n;
+}
+
+template <typename T, int VE, int NV, bool kFull>
+cudaError_t run_shape(Pass pass, NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
   a.tpr = s.tpr;
-  const int grid = grid_for(a.tokens * a.heads, s);
-  const size_t sh = a.partial && s.groups > 1 ? (size_t)s.groups * 2 * a.D * sizeof(float) : 0;
-  if (a.codes) norm_bwd_kernel<T, VE, true><<<grid, s.threads, sh, st>>>(a);
-  else norm_bwd_kernel<T, VE, false><<<grid, s.threads, sh, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  if (pass != kBackward) {
+    constexpr int n = batch_rows(sizeof(T), VE * NV, false);
+    return batched(a.rows, s, n) ? run_rows<T, VE, NV, n, kFull>(pass, a, s, st)
+                                        : run_rows<T, VE, NV, 1, kFull>(pass, a, s, st);
+  }
+  constexpr int n = batch_rows(sizeof(T), VE * NV, true);
+  const bool many = batched(a.rows, s, n);
+  cudaError_t e = many ? run_rows<T, VE, NV, n, kFull>(pass, a, s, st) : run_rows<T, VE, NV, 1, kFull>(pass, a, s, st);
   if (e != cudaSuccess || !a.partial) return e;
-  norm_fold_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(a.partial, grid, a.D, dW, db);
+  const int parts = grid_for(a.rows, s, many ? n : 1);
+  norm_fold_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(a.partial, parts, a.D, dW, db);
   return cudaGetLastError();
 }
 
+template <typename T, int VE, int NV>
+cudaError_t run_per(Pass pass, NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
+  // Single elements are the path of odd widths: kept to one variant.
+  if constexpr (VE > 1) {
+    if (s.full) return run_shape<T, VE, NV, true>(pass, a, s, dW, db, st);
+  }
+  return run_shape<T, VE, NV, false>(pass, a, s, dW, db, st);
+}
+
 template <typename T, int VE>
-cudaError_t apply(NormArgs a, cudaStream_t st) {
+cudaError_t run_wide(Pass pass, NormArgs& a, float* dW, float* db, cudaStream_t st) {
   const Shape s = shape_for(a.D, VE);
-  a.tpr = s.tpr;
-  norm_apply_kernel<T, VE><<<grid_for(a.tokens * a.heads, s), s.threads, 0, st>>>(a);
-  return cudaGetLastError();
+  if (s.per == 8) return run_per<T, VE, 8 / VE>(pass, a, s, dW, db, st);
+  if (s.per == 16) return run_per<T, VE, 16 / VE>(pass, a, s, dW, db, st);
+  return run_per<T, VE, 32 / VE>(pass, a, s, dW, db, st);
+}
+
+cudaError_t run(Pass pass, int dtype, NormArgs& a, float* dW, float* db, cudaStream_t st) {
+  using bf = __nv_bfloat16;
+  if (dtype == VDA_DTYPE_BF16)
+    return wide<bf>(a) ? run_wide<bf, 8>(pass, a, dW, db, st) : run_wide<bf, 1>(pass, a, dW, db, st);
+  return wide<float>(a) ? run_wide<float, 4>(pass, a, dW, db, st) : run_wide<float, 1>(pass, a, dW, db, st);
 }
 
 NormArgs args_for(const vda_norm_problem& p) {
   NormArgs a{};
-  a.tokens = p.tokens;
+  a.rows = p.tokens * p.heads;
   a.heads = p.heads;
   a.D = p.D;
-  a.ld_x = p.ld_x ? p.ld_x : (int64_t)p.heads * p.D;
-  a.ld_y = p.ld_y ? p.ld_y : (int64_t)p.heads * p.D;
+  const int64_t dense = (int64_t)p.heads * p.D;
+  a.ld_x = p.ld_x ? p.ld_x : dense;
+  a.ld_y = p.ld_y ? p.ld_y : dense;
   // Tokens without gaps are rows like any others.
-  if (a.ld_x == (int64_t)p.heads * p.D && a.ld_y == a.ld_x) {
-    a.tokens *= p.heads;
+  if (a.ld_x == dense && a.ld_y == dense) {
     a.heads = 1;
     a.ld_x = a.ld_y = p.D;
   }
+  a.by_heads = a.heads > 1 ? ~0ull / (uint64_t)a.heads + 1 : 0;
   a.eps = p.eps;
   a.inv_d = 1.f / (float)p.D;
   a.w_bf16 = p.w_dtype == VDA_DTYPE_BF16;
@@ -446,7 +735,7 @@ size_t norm_backward_workspace_bytes(const vda_norm_problem& p) {
   if (rows == 0) return 0;
   int parts = 0;
   for (int ve : {1, 4, 8}) {
-    const int g = grid_for(rows, shape_for(p.D, ve));
+    const int g = grid_for(rows, shape_for(p.D, ve), 1);
     parts = g > parts ? g : parts;
   }
   return align_up((size_t)parts * 2 * p.D * sizeof(float), 256);
@@ -455,7 +744,7 @@ size_t norm_backward_workspace_bytes(const vda_norm_problem& p) {
 cudaError_t launch_layer_norm(const vda_norm_problem& p, const void* X, const void* W, const void* bias, void* Y,
                               float* mean, float* rstd, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   NormArgs a = args_for(p);
-  if (a.tokens == 0) return cudaSuccess;
+  if (a.rows == 0) return cudaSuccess;
   a.X = X;
   a.W = W;
   a.bias = bias;
@@ -464,16 +753,14 @@ cudaError_t launch_layer_norm(const vda_norm_problem& p, const void* X, const vo
   a.rstd = rstd;
   a.codes = codes;
   a.scales = scales;
-  if (p.dtype == VDA_DTYPE_BF16)
-    return wide<__nv_bfloat16>(a) ? fwd<__nv_bfloat16, 8>(a, st) : fwd<__nv_bfloat16, 1>(a, st);
-  return wide<float>(a) ? fwd<float, 4>(a, st) : fwd<float, 1>(a, st);
+  return run(kForward, p.dtype, a, nullptr, nullptr, st);
 }
 
 cudaError_t launch_layer_norm_backward(const vda_norm_problem& p, const void* dY, const void* X, const float* mean,
                                        const float* rstd, const uint8_t* codes, const uint8_t* scales, const void* W,
                                        void* dX, float* dW, float* db, float* partial, cudaStream_t st) {
   NormArgs a = args_for(p);
-  if (a.tokens == 0) {
+  if (a.rows == 0) {
     cudaError_t e = dW ? cudaMemsetAsync(dW, 0, (size_t)p.D * sizeof(float), st) : cudaSuccess;
     if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, (size_t)p.D * sizeof(float), st);
     return e;
@@ -487,23 +774,19 @@ cudaError_t launch_layer_norm_backward(const vda_norm_problem& p, const void* dY
   a.codes = const_cast<uint8_t*>(codes);
   a.scales = const_cast<uint8_t*>(scales);
   a.partial = dW || db ? partial : nullptr;
-  if (p.dtype == VDA_DTYPE_BF16)
-    return wide<__nv_bfloat16>(a) ? bwd<__nv_bfloat16, 8>(a, dW, db, st) : bwd<__nv_bfloat16, 1>(a, dW, db, st);
-  return wide<float>(a) ? bwd<float, 4>(a, dW, db, st) : bwd<float, 1>(a, dW, db, st);
+  return run(kBackward, p.dtype, a, dW, db, st);
 }
 
 cudaError_t launch_layer_norm_from_checkpoint(const vda_norm_problem& p, const uint8_t* codes, const uint8_t* scales,
                                               const void* W, const void* bias, void* Y, cudaStream_t st) {
   NormArgs a = args_for(p);
-  if (a.tokens == 0) return cudaSuccess;
+  if (a.rows == 0) return cudaSuccess;
   a.W = W;
   a.bias = bias;
   a.Y = Y;
   a.codes = const_cast<uint8_t*>(codes);
   a.scales = const_cast<uint8_t*>(scales);
-  if (p.dtype == VDA_DTYPE_BF16)
-    return wide<__nv_bfloat16>(a) ? apply<__nv_bfloat16, 8>(a, st) : apply<__nv_bfloat16, 1>(a, st);
-  return wide<float>(a) ? apply<float, 4>(a, st) : apply<float, 1>(a, st);
+  return run(kApply, p.dtype, a, nullptr, nullptr, st);
 }
 
 }  // namespace vda

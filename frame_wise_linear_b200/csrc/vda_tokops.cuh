@@ -24,6 +24,7 @@ constexpr int kBlock = 32;   // elements that share a scale
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(uint8_t x) { return (float)x; }
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
 template <>
@@ -33,6 +34,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 
 template <int Bytes>
 struct RawOf;
+template <> struct RawOf<1> { using type = uint8_t; };
 template <> struct RawOf<2> { using type = uint16_t; };
 template <> struct RawOf<4> { using type = uint32_t; };
 template <> struct RawOf<8> { using type = uint2; };
@@ -47,15 +49,23 @@ struct Pack {
     Raw raw;
     T e[VE];
   };
-  __device__ Pack() {}
+  __device__ __forceinline__ Pack() {}
   __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < VE; ++i) e[i] = from_f32<T>(0.f);
-  }
+  __device__ __forceinline__ void zero() { raw = Raw{}; }
   __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
   __device__ __forceinline__ void set(int i, float x) { e[i] = from_f32<T>(x); }
+  // Elements i and i + 1 (i even) in one conversion.
+  __device__ __forceinline__ void set2(int i, float2 v) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 b = __float22bfloat162_rn(v);
+      e[i] = b.x;
+      e[i + 1] = b.y;
+    } else {
+      e[i] = from_f32<T>(v.x);
+      e[i + 1] = from_f32<T>(v.y);
+    }
+  }
 };
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
@@ -93,19 +103,44 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The largest of v over groups of `lanes` neighbouring lanes (a power of two
-// up to 32); every lane of the warp takes part.
+// Two float32 at a time: one instruction each on this architecture.
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+  return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 from_bits2(uint64_t b) {
+  return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return from_bits2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return from_bits2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return from_bits2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The largest of v over groups of Lanes neighbouring lanes (a power of two up
+// to 32); the lanes of a group take part together.
 template <int Lanes>
 __device__ __forceinline__ float lanes_max(float v) {
+  const uint32_t group = (uint32_t)((1ull << Lanes) - 1) << ((threadIdx.x & 31) / Lanes * Lanes);
 #pragma unroll
-  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(group, v, o));
   return v;
 }
 
 // VE values to codes, and the block's scale byte, by the 32 / VE neighbouring
 // lanes that hold the block (values beyond the row are 0).
 template <int VE>
-__device__ __forceinline__ int encode_block(const float (&x)[VE], uint8_t (&codes)[VE]) {
+__device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, VE>& codes) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < VE; ++i) top = fmaxf(top, block_mag(x[i]));
@@ -113,63 +148,49 @@ __device__ __forceinline__ int encode_block(const float (&x)[VE], uint8_t (&code
   const int s = scale_byte(top);
   const float inv = inv_scale_of(s);
   if (VE == 1) {
-    codes[0] = (uint8_t)encode2(x[0], 0.f, inv, s);
+    codes.e[0] = (uint8_t)encode2(x[0], 0.f, inv, s);
   } else {
 #pragma unroll
     for (int i = 0; i + 1 < VE; i += 2) {
       const uint32_t two = encode2(x[i], x[i + 1], inv, s);
-      codes[i] = (uint8_t)two;
-      codes[i + 1] = (uint8_t)(two >> 8);
+      codes.e[i] = (uint8_t)two;
+      codes.e[i + 1] = (uint8_t)(two >> 8);
     }
   }
   return s;
 }
 
-// VE codes in one store or load (VE 1, 4 or 8 bytes, aligned to that).
+// The values of VE neighbouring codes at one scale.
 template <int VE>
-__device__ __forceinline__ void store_codes(uint8_t* p, const uint8_t (&c)[VE]) {
-  if constexpr (VE == 8) {
-    uint2 r;
-    r.x = c[0] | c[1] << 8 | c[2] << 16 | (uint32_t)c[3] << 24;
-    r.y = c[4] | c[5] << 8 | c[6] << 16 | (uint32_t)c[7] << 24;
-    *reinterpret_cast<uint2*>(p) = r;
-  } else if constexpr (VE == 4) {
-    *reinterpret_cast<uint32_t*>(p) = c[0] | c[1] << 8 | c[2] << 16 | (uint32_t)c[3] << 24;
+__device__ __forceinline__ void decode_pack(const Pack<uint8_t, VE>& c, float scale, float (&x)[VE]) {
+  if constexpr (VE == 1) {
+    x[0] = decode2(c.e[0]).x * scale;
   } else {
-    static_assert(VE == 1, "1, 4 or 8 codes");
-    *p = c[0];
+#pragma unroll
+    for (int i = 0; i < VE; i += 2) {
+      const float2 v = decode2(c.e[i] | (uint32_t)c.e[i + 1] << 8);
+      x[i] = v.x * scale;
+      x[i + 1] = v.y * scale;
+    }
   }
 }
 
-// The codes of VE neighbouring elements as loaded; values() scales them.
-template <int VE>
-struct CodePack {
-  uint32_t w[VE > 4 ? 2 : 1];
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (VE == 8) {
-      const uint2 r = *reinterpret_cast<const uint2*>(p);
-      w[0] = r.x;
-      w[1] = r.y;
-    } else if constexpr (VE == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      static_assert(VE == 1, "1, 4 or 8 codes");
-      w[0] = *p;
-    }
-  }
-  __device__ __forceinline__ void values(float scale, float (&x)[VE]) const {
-    if constexpr (VE == 1) {
-      x[0] = decode2(w[0]).x * scale;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; i += 2) {
-        const float2 v = decode2((w[i / 4] >> (8 * (i % 4))) & 0xffffu);
-        x[i] = v.x * scale;
-        x[i + 1] = v.y * scale;
-      }
-    }
-  }
-};
+// Asynchronous copies of 4, 8 or 16 bytes into shared memory, in groups that
+// complete in order; both addresses are multiples of the size.
+template <int Bytes>
+__device__ __forceinline__ void async_copy(void* shared, const void* global) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(shared));
+  if constexpr (Bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(global), "n"(Bytes) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups are still on their way.
+template <int N>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 }  // namespace tokops
 }  // namespace vda
