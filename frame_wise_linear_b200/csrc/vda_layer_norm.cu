@@ -72,9 +72,16 @@ __device__ __forceinline__ float load_w(const void* w, int i, int w_bf16) {
 // Sums over a group of neighbouring lanes (lanes: a power of two).
 template <int N>
 __device__ __forceinline__ void lanes_sum(float (&v)[N], int lanes) {
-  for (int o = lanes / 2; o > 0; o >>= 1) {
+  if (lanes == 32) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  } else {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    }
   }
 }
 __device__ __forceinline__ float half_warp_sum(float v) {
@@ -201,15 +208,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
   const T* X = static_cast<const T*>(a.X);
   // Row r of a batch that starts at row0: row0 + r groups + group.
   const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
-  auto fetch = [&](int buf, int64_t row0) {
+  auto fetch = [&](int buf, int64_t row0, auto whole) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
-      if (row < a.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
+      if (decltype(whole)::value || row < a.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
     }
   };
   int64_t row0 = blockIdx.x * span;
-  fetch(0, row0);
+  fetch(0, row0, std::false_type());
   async_commit();
   Pairs<N> w, b;
   load_columns(a.W, a, p, 1.f, w);
@@ -221,16 +228,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
   const int peer = p.lane & 15;
   const bool in_row = peer < p.warps;
   const float weight = in_row ? (float)p.warp_elements(peer) * a.inv_d : 0.f;
-  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
-    fetch(buf ^ 1, row0 + step);
-    async_commit();
-    async_wait<1>();
+  auto body = [&](int buf, int64_t row0, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
     float mean[kRows], rstd[kRows], s[kRows], m2[kRows], own[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
       s[r] = m2[r] = own[r] = 0.f;
-      if (row < a.rows) {
+      if (kWhole || row < a.rows) {
         Pairs<N> x;
         in.get(buf, r, X + row_at(a, row, a.ld_x), p, x);
         float2 sum = x.p[0];
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
-      if (row >= a.rows) break;
+      if (!kWhole && row >= a.rows) break;
       const T* xr = X + row_at(a, row, a.ld_x);
       T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
       Pairs<N> x, y;
@@ -327,6 +332,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
         if (a.rstd) a.rstd[row] = rstd[r];
       }
     }
+  };
+  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+    if (row0 + step + span <= a.rows) fetch(buf ^ 1, row0 + step, std::true_type());
+    else fetch(buf ^ 1, row0 + step, std::false_type());
+    async_commit();
+    async_wait<1>();
+    // All but a batch that the rows' end cuts off need no test of each row.
+    if (row0 + span <= a.rows) body(buf, row0, std::true_type());
+    else body(buf, row0, std::false_type());
   }
 }
 
@@ -377,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
   float mean[kRows], rstd[kRows], next_mean[kRows], next_rstd[kRows];
   int sb[kRows][kSb], next_sb[kRows][kSb];
   const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
-  auto fetch = [&](int buf, int64_t row0) {
+  auto fetch = [&](int buf, int64_t row0, auto whole) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
-      if (row < a.rows) {
+      if (decltype(whole)::value || row < a.rows) {
         iny.fetch(buf, r, dY + row_at(a, row, a.ld_y), p);
         inx.fetch(buf, r, X + x_at(row), p);
         next_rstd[r] = a.rstd[row];
@@ -408,29 +422,20 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
     for (int k = 0; k < kSb; ++k) next_sb[r][k] = 0;
   }
   int64_t row0 = blockIdx.x * span;
-  fetch(0, row0);
+  fetch(0, row0, std::false_type());
   async_commit();
   Pairs<N> w, dw, db;
   load_columns(a.W, a, p, 1.f, w);
 #pragma unroll
   for (int j = 0; j < N / 2; ++j) dw.p[j] = db.p[j] = both(0.f);
-  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      mean[r] = next_mean[r];
-      rstd[r] = next_rstd[r];
-#pragma unroll
-      for (int k = 0; k < kSb; ++k) sb[r][k] = next_sb[r][k];
-    }
-    fetch(buf ^ 1, row0 + step);
-    async_commit();
-    async_wait<1>();
+  auto body = [&](int buf, int64_t row0, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
     float s[2 * kRows];   // of g, then of g xh
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
       float2 s1 = both(0.f), s2 = both(0.f);
-      if (row < a.rows) {
+      if (kWhole || row < a.rows) {
         Pairs<N> dy, xh;
         get(buf, r, row, dy, xh);
         // Where the thread has no vector dy is 0: nothing is added.
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = row0 + r * p.groups + p.group;
-      if (row >= a.rows) break;
+      if (!kWhole && row >= a.rows) break;
       T* dx = static_cast<T*>(a.Y) + row_at(a, row, a.ld_x);
       const float2 c1 = both(-s[r] * a.inv_d), c2 = both(-s[kRows + r] * a.inv_d), rs = both(rstd[r]);
       Pairs<N> dy, xh;
@@ -483,6 +488,21 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
         if (p.has(k)) d.store(dx + p.vec(k) * VE);
       }
     }
+  };
+  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      mean[r] = next_mean[r];
+      rstd[r] = next_rstd[r];
+#pragma unroll
+      for (int k = 0; k < kSb; ++k) sb[r][k] = next_sb[r][k];
+    }
+    if (row0 + step + span <= a.rows) fetch(buf ^ 1, row0 + step, std::true_type());
+    else fetch(buf ^ 1, row0 + step, std::false_type());
+    async_commit();
+    async_wait<1>();
+    if (row0 + span <= a.rows) body(buf, row0, std::true_type());
+    else body(buf, row0, std::false_type());
   }
   if (!a.partial) return;
   float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
