@@ -574,8 +574,8 @@ vda_status check_checkpoint(const vda_checkpoint_problem* p, const void* X, cons
     return fail(VDA_ERR_INVALID_ARG, "rows must be in [0, 2^40] (got %lld)", (long long)p->rows);
   if (p->D < 1) return fail(VDA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", p->D);
   if (p->D > (1 << 24)) return fail(VDA_ERR_UNSUPPORTED, "D up to 2^24 is supported (got %d)", p->D);
-  if (p->rows > 0 && p->D >= (1LL << 46) / p->rows + ((1LL << 46) % p->rows != 0))
-    return fail(VDA_ERR_UNSUPPORTED, "rows * D must be below 2^46");
+  if (p->rows > ((1LL << 36) - 1) / ((p->D + 31) / 32))
+    return fail(VDA_ERR_UNSUPPORTED, "rows * ceil(D / 32) must be below 2^36");
   if (!float_type(p->dtype)) return fail(VDA_ERR_INVALID_ARG, "dtype must be float32 or bfloat16 (got %d)", p->dtype);
   VDA_CHECK(check_stride(p->ld, p->D, "ld"));
   if (p->rows > 0) {

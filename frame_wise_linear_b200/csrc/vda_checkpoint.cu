@@ -14,51 +14,94 @@ namespace {
 
 using namespace tokops;
 
-// Units of VE elements, row by row, each row's count rounded up to whole
-// blocks so that a block never straddles two warps.
+// A unit is VE elements of a row; a row's count is rounded up to whole blocks,
+// so that a block's lanes are neighbours in one warp.
+struct Rows {
+  int64_t units;      // of all rows
+  int per_row;        // units of a row
+  uint64_t by;        // ceil(2^64 / per_row) where the quotient by it is exact, else 0
+  int64_t ld;         // of the tensor
+  int D, nblk;
+  int whole;          // codes and tensor are dense and D is whole blocks: unit u is elements u VE ..
+};
+
+template <int VE>
+struct Unit {
+  int64_t row;
+  int v;
+  bool in;
+  int64_t at, code, scale;   // element offsets in the tensor and the codes, and the scale byte's
+  __device__ __forceinline__ Unit(const Rows& r, int64_t u) {
+    if (r.whole) {
+      in = u < r.units;
+      at = code = u * VE;
+      scale = u / (kBlock / VE);
+      return;
+    }
+    row = r.by ? (int64_t)__umul64hi((uint64_t)u, r.by) : u / r.per_row;
+    v = (int)(u - row * r.per_row);
+    in = u < r.units && v * VE < r.D;
+    at = row * r.ld + v * VE;
+    code = row * r.D + v * VE;
+    scale = row * r.nblk + v / (kBlock / VE);
+  }
+};
+
+constexpr int kUnits = 4;   // of a thread, all on their way before the first is used
+
 template <typename T, int VE>
-__global__ void __launch_bounds__(256) pack_kernel(const T* X, int64_t rows, int D, int64_t ld, uint8_t* codes,
-                                                   uint8_t* scales) {
-  const int nblk = (D + kBlock - 1) / kBlock;
-  const int per_row = nblk * (kBlock / VE);
-  const int64_t units = rows * per_row;
-  for (int64_t u0 = (int64_t)blockIdx.x * blockDim.x; u0 < units; u0 += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t u = u0 + threadIdx.x;
-    const int64_t row = u / per_row;
-    const int v = (int)(u - row * per_row);
-    const bool in = u < units && v * VE < D;
-    Pack<T, VE> q;
-    if (in) q.load(X + row * ld + (int64_t)v * VE);
-    else q.zero();
+__global__ void __launch_bounds__(256) pack_kernel(const T* X, const Rows r, uint8_t* codes, uint8_t* scales) {
+  const int64_t u0 = (int64_t)blockIdx.x * (256 * kUnits) + threadIdx.x;
+  Pack<T, VE> q[kUnits];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const Unit<VE> u(r, u0 + j * 256);
+    q[j].zero();
+    if (u.in) q[j].load(X + u.at);
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const Unit<VE> u(r, u0 + j * 256);
     float x[VE];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = q.get(i);
+    for (int i = 0; i < VE; ++i) x[i] = q[j].get(i);
     Pack<uint8_t, VE> c;
     const int s = encode_block<VE>(x, c);
-    if (in) {
-      c.store(codes + row * D + (int64_t)v * VE);
-      if (v % (kBlock / VE) == 0) scales[row * nblk + v / (kBlock / VE)] = (uint8_t)s;
+    if (u.in) {
+      c.store(codes + u.code);
+      if (threadIdx.x % (kBlock / VE) == 0) scales[u.scale] = (uint8_t)s;
     }
   }
 }
 
 template <typename T, int VE>
-__global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows, int D,
-                                                     int64_t ld, T* X) {
-  const int nblk = (D + kBlock - 1) / kBlock;
-  const int per_row = D / VE;
-  const int64_t units = rows * per_row;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = u / per_row;
-    const int v = (int)(u - row * per_row);
-    Pack<uint8_t, VE> c;
-    float x[VE];
-    c.load(codes + row * D + (int64_t)v * VE);
-    decode_pack<VE>(c, scale_of(scales[row * nblk + v / (kBlock / VE)]), x);
-    Pack<T, VE> q;
+__global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* codes, const uint8_t* scales, const Rows r, T* X) {
+  const int64_t u0 = (int64_t)blockIdx.x * (256 * kUnits) + threadIdx.x;
+  Pack<uint8_t, VE> c[kUnits];
+  int s[kUnits];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) q.set(i, x[i]);
-    q.store(X + row * ld + (int64_t)v * VE);
+  for (int j = 0; j < kUnits; ++j) {
+    const Unit<VE> u(r, u0 + j * 256);
+    c[j].zero();
+    s[j] = 0;
+    if (u.in) {
+      c[j].load(codes + u.code);
+      s[j] = scales[u.scale];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const Unit<VE> u(r, u0 + j * 256);
+    float x[VE];
+    decode_pack<VE>(c[j], scale_of(s[j]), x);
+    Pack<T, VE> q;
+    if constexpr (VE > 1) {
+#pragma unroll
+      for (int i = 0; i < VE; i += 2) q.set2(i, make_float2(x[i], x[i + 1]));
+    } else {
+      q.set(0, x[0]);
+    }
+    if (u.in) q.store(X + u.at);
   }
 }
 
@@ -70,24 +113,35 @@ bool wide(const void* X, const void* codes, int D, int64_t ld) {
   return D % ve == 0 && ld % ve == 0 && aligned_to(X, 16) && aligned_to(codes, ve);
 }
 
-int grid_for(int64_t units) {
-  const int64_t b = (units + 255) / 256;
-  return (int)(b < 148 * 64 ? b : 148 * 64);
+Rows rows_for(const vda_checkpoint_problem& p, int64_t ld, int ve) {
+  Rows r{};
+  r.nblk = (p.D + kBlock - 1) / kBlock;
+  r.per_row = r.nblk * (kBlock / ve);
+  r.units = p.rows * r.per_row;
+  r.ld = ld;
+  r.D = p.D;
+  r.whole = ld == p.D && p.D % kBlock == 0;
+  // u * ceil(2^64 / n) >> 64 = u / n while u n < 2^64.
+  if (r.per_row > 1 && r.units <= (1LL << 62) / r.per_row) r.by = ~0ull / (uint64_t)r.per_row + 1;
+  return r;
 }
+
+// CTAs of 256 threads: below 2^31, as there are fewer than 2^36 blocks of at most 32 units.
+unsigned grid_for(const Rows& r) { return (unsigned)((r.units + 256 * kUnits - 1) / (256 * kUnits)); }
 
 template <typename T, int VE>
 cudaError_t pack(const vda_checkpoint_problem& p, const void* X, uint8_t* codes, uint8_t* scales, int64_t ld,
                  cudaStream_t st) {
-  const int64_t units = p.rows * ((p.D + kBlock - 1) / kBlock * (kBlock / VE));
-  pack_kernel<T, VE><<<grid_for(units), 256, 0, st>>>(static_cast<const T*>(X), p.rows, p.D, ld, codes, scales);
+  const Rows r = rows_for(p, ld, VE);
+  pack_kernel<T, VE><<<grid_for(r), 256, 0, st>>>(static_cast<const T*>(X), r, codes, scales);
   return cudaGetLastError();
 }
 
 template <typename T, int VE>
 cudaError_t unpack(const vda_checkpoint_problem& p, const uint8_t* codes, const uint8_t* scales, void* X, int64_t ld,
                    cudaStream_t st) {
-  unpack_kernel<T, VE><<<grid_for(p.rows * (p.D / VE)), 256, 0, st>>>(codes, scales, p.rows, p.D, ld,
-                                                                    static_cast<T*>(X));
+  const Rows r = rows_for(p, ld, VE);
+  unpack_kernel<T, VE><<<grid_for(r), 256, 0, st>>>(codes, scales, r, static_cast<T*>(X));
   return cudaGetLastError();
 }
 

@@ -85,17 +85,19 @@ __device__ __forceinline__ int scale_byte(float top) {
 __device__ __forceinline__ float scale_of(int s) { return __uint_as_float(s ? (uint32_t)s << 23 : 0x400000u); }
 __device__ __forceinline__ float inv_scale_of(int s) { return __uint_as_float((uint32_t)(254 - s) << 23); }
 
-// Two scaled values to two codes (x in the low byte).  At the largest scale
-// byte, 247, a scaled value of 248 or more would round to 256, which stands
-// for 2^128: 240 is taken, within the same half step of 2^-4.
-__device__ __forceinline__ uint32_t encode2(float x, float y, float inv, int s) {
-  x = finite(x) ? x * inv : __uint_as_float(0x7fffffffu);
-  y = finite(y) ? y * inv : __uint_as_float(0x7fffffffu);
-  if (s >= 247) {
-    x = x > 240.f ? 240.f : (x < -240.f ? -240.f : x);
-    y = y > 240.f ? 240.f : (y < -240.f ? -240.f : y);
-  }
-  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+// Two scaled values to two codes (x in the low byte); NaN stays NaN.
+__device__ __forceinline__ uint32_t encode2(float2 v) {
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+// The same for any values of a block with scale byte s: infinities become NaN,
+// and at the largest scale byte, 247, where a scaled value of 248 or more
+// would round to 256, which stands for 2^128, 240 is taken, within the same
+// half step of 2^-4.
+__device__ __forceinline__ uint32_t encode2_any(float2 v, float inv, int s) {
+  const float nan = __uint_as_float(0x7fffffffu), most = s >= 247 ? 240.f : 448.f;
+  v.x = finite(v.x) ? fminf(fmaxf(v.x * inv, -most), most) : nan;
+  v.y = finite(v.y) ? fminf(fmaxf(v.y * inv, -most), most) : nan;
+  return encode2(v);
 }
 // The values of two codes, unscaled (exact).
 __device__ __forceinline__ float2 decode2(uint32_t two) {
@@ -137,26 +139,36 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+// From here up (448 * 2^119: infinity among them) a block takes encode2_any.
+constexpr float kLargeTop = 448.f * 0x1p119f;
+
 // VE values to codes, and the block's scale byte, by the 32 / VE neighbouring
-// lanes that hold the block (values beyond the row are 0).
+// lanes that hold the block (values beyond the row are 0).  fmaxf passes over
+// NaN, so a block without infinities needs no test of its elements.
 template <int VE>
 __device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, VE>& codes) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < VE; ++i) top = fmaxf(top, block_mag(x[i]));
+  for (int i = 0; i < VE; ++i) top = fmaxf(top, fabsf(x[i]));
   top = lanes_max<kBlock / VE>(top);
-  const int s = scale_byte(top);
-  const float inv = inv_scale_of(s);
-  if (VE == 1) {
-    codes.e[0] = (uint8_t)encode2(x[0], 0.f, inv, s);
-  } else {
+  int s = scale_byte(top);
+  uint32_t two[VE > 1 ? VE / 2 : 1];
+  if (top <= kLargeTop) {
+    const float2 inv = both(inv_scale_of(s));
 #pragma unroll
-    for (int i = 0; i + 1 < VE; i += 2) {
-      const uint32_t two = encode2(x[i], x[i + 1], inv, s);
-      codes.e[i] = (uint8_t)two;
-      codes.e[i + 1] = (uint8_t)(two >> 8);
-    }
+    for (int i = 0; i < VE; i += 2) two[i / 2] = encode2(mul2(make_float2(x[i], VE > 1 ? x[i + 1] : 0.f), inv));
+  } else {
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) top = fmaxf(top, block_mag(x[i]));
+    top = lanes_max<kBlock / VE>(top);
+    s = scale_byte(top);
+#pragma unroll
+    for (int i = 0; i < VE; i += 2)
+      two[i / 2] = encode2_any(make_float2(x[i], VE > 1 ? x[i + 1] : 0.f), inv_scale_of(s), s);
   }
+#pragma unroll
+  for (int i = 0; i < VE; ++i) codes.e[i] = (uint8_t)(two[i / 2] >> (8 * (i % 2)));
   return s;
 }
 
@@ -168,9 +180,9 @@ __device__ __forceinline__ void decode_pack(const Pack<uint8_t, VE>& c, float sc
   } else {
 #pragma unroll
     for (int i = 0; i < VE; i += 2) {
-      const float2 v = decode2(c.e[i] | (uint32_t)c.e[i + 1] << 8);
-      x[i] = v.x * scale;
-      x[i + 1] = v.y * scale;
+      const float2 v = mul2(decode2(c.e[i] | (uint32_t)c.e[i + 1] << 8), both(scale));
+      x[i] = v.x;
+      x[i + 1] = v.y;
     }
   }
 }

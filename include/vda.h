@@ -441,7 +441,7 @@ vda_status vda_rope_backward(const vda_rope_problem* p, const void* dQ_rot, cons
  * 2^-4 |x|, or 2^-10 * 2^e where that is more.  (Magnitudes from 248 * 2^120 up
  * take 240 * 2^120, so that unpacking stays finite.)  NaN and infinities are kept as
  * NaN and leave the rest of their block alone.
- * rows in [0, 2^40], D in [1, 2^24], rows * D < 2^46; ld: elements from one
+ * rows in [0, 2^40], D in [1, 2^24], rows * ceil(D / 32) < 2^36; ld: elements from one
  * row of the tensor to the next (0: D; else at least D and below 2^31);
  * codes and scales are dense. */
 typedef struct vda_checkpoint_problem {
