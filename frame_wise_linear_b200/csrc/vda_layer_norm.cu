@@ -533,21 +533,28 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
 }
 
 // dW and db from the CTAs' partial sums [parts][2 D]: 32 columns a block,
-// thread (x, y) adds rows y, y + 8, ...; then the 8 sums of a column in order.
-__global__ void __launch_bounds__(256) norm_fold_kernel(const float* partial, int parts, int D, float* dW, float* db) {
-  __shared__ float sh[8][33];
+// thread (x, y) adds rows y, y + 32, ...; then a warp the 32 sums of a column.  The rows come from L2; there are at most 296 of them, so a thread
+// has ten loads, all on their way at once.
+__global__ void __launch_bounds__(1024) norm_fold_kernel(const float* partial, int parts, int D, float* dW, float* db) {
+  __shared__ float sh[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   float v = 0.f;
-  if (c < 2 * D)
-    for (int i = y; i < parts; i += 8) v += partial[(int64_t)i * 2 * D + c];
+  if (c < 2 * D) {
+#pragma unroll 10
+    for (int i = y; i < parts; i += 32) v += partial[(int64_t)i * 2 * D + c];
+  }
   sh[y][x] = v;
   __syncthreads();
-  if (y == 0 && c < 2 * D) {
-    for (int i = 1; i < 8; ++i) v += sh[i][x];
-    if (c < D) {
-      if (dW) dW[c] = v;
+  // Warp y adds column y's 32 sums.
+  v = sh[x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + y;
+  if (x == 0 && col < 2 * D) {
+    if (col < D) {
+      if (dW) dW[col] = v;
     } else if (db) {
-      db[c - D] = v;
+      db[col - D] = v;
     }
   }
 }
@@ -699,7 +706,7 @@ cudaError_t run_shape(Pass pass, NormArgs& a, const Shape& s, float* dW, float* 
   cudaError_t e = many ? run_rows<T, VE, NV, n, kFull>(pass, a, s, st) : run_rows<T, VE, NV, 1, kFull>(pass, a, s, st);
   if (e != cudaSuccess || !a.partial) return e;
   const int parts = grid_for(a.rows, s, many ? n : 1);
-  norm_fold_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(a.partial, parts, a.D, dW, db);
+  norm_fold_kernel<<<(2 * a.D + 31) / 32, 1024, 0, st>>>(a.partial, parts, a.D, dW, db);
   return cudaGetLastError();
 }
 

@@ -8,11 +8,13 @@
 // The other channels are copied.  The turn is orthogonal, so the gradients
 // are the gradients of the output turned back (sin negated).
 //
-// Bound by HBM: every element of Q and K is read and written once.  A thread
-// takes one unit of a token (a vector of VE channels and, where pairs are
-// half the width apart, its partner vector), computes that unit's sines and
-// cosines once and applies them in every head of Q and K, so they cost one
-// evaluation per 2 (H_q + H_k) elements moved and stay in registers.
+// Bound by HBM: every element of Q and K is read and written once.  A CTA takes
+// a tile of tokens in all heads of Q and K: it computes the tile's cosines and
+// sines once, into shared memory, while its first loads are on their way.  A
+// thread then stays with one unit of one token (a vector of VE channels and,
+// where pairs are half the width apart, its partner vector), holds that unit's
+// cosines and sines in registers and walks over heads, the next kAhead heads
+// on their way while it turns the last ones.
 //
 // Angles.  position x frequency is formed in turns (frequencies divided by
 // 2 pi in double on the host) and in double: at position 10^6 a float32
@@ -35,10 +37,10 @@ struct RopeArgs {
   void* out[2];
   const float* positions;   // [B][N][3], or null: the grid's
   int64_t ld_in[2], ld_out[2];   // token-major: elements between tokens
-  int64_t N;            // tokens per batch item
-  int64_t threads;      // B N units
+  uint32_t N, tokens;   // per batch item, and of all: below 2^31
   int heads[2];         // H_q, H_k
-  int d, rot, units, layout, chunk;   // chunk: heads a thread takes (of H_q + H_k)
+  int d, rot, units, layout;
+  int tile, lanes;      // tokens of a CTA; threads that share a unit of a token, each with every lanes-th head
   int first[3];         // pairs before axis 1, before axis 2, in all
   int height, width;
   float sign;           // -1: the gradients
@@ -46,157 +48,166 @@ struct RopeArgs {
   double turns[kMaxPairs];   // frequency / (2 pi) per pair
 };
 
-// kHalves: pair j is channels (j, j + rot / 2); a unit is VE of the first and
-// their partners, or VE channels behind the turned ones.  Otherwise pair j is
-// channels (2 j, 2 j + 1), a unit VE neighbouring channels (VE even).
-template <typename T, int VE, bool kHalves>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int NP = kHalves ? VE : (VE + 1) / 2;   // pairs of a unit
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= a.threads) return;
-  const int64_t token = id / a.units;   // over all batch items
-  const int unit = (int)(id - token * a.units);
-  const int64_t item = token / a.N, tok = token - item * a.N;
-  double pos[3];
+// Cosine and sine of pair j at a token.
+__device__ __forceinline__ float2 turn_of(const RopeArgs& a, uint32_t token, int j) {
+  const int axis = j >= a.first[1] ? 2 : (j >= a.first[0] ? 1 : 0);
+  double pos;
   if (a.positions) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) pos[i] = (double)a.positions[token * 3 + i];
+    pos = (double)a.positions[(int64_t)token * 3 + axis];
   } else {
-    const int64_t row = tok / a.width;
-    const int64_t t = row / a.height;
-    pos[0] = a.pos0[0] + a.step[0] * (double)t;
-    pos[1] = a.pos0[1] + a.step[1] * (double)(row - t * a.height);
-    pos[2] = a.pos0[2] + a.step[2] * (double)(tok - row * a.width);
+    const uint32_t tok = token % a.N, row = tok / (uint32_t)a.width, t = row / (uint32_t)a.height;
+    const uint32_t i = axis == 0 ? t : (axis == 1 ? row - t * a.height : tok - row * a.width);
+    pos = a.pos0[axis] + a.step[axis] * (double)i;
   }
-  const int half = a.rot / 2;
-  // Channels of the unit, and of its partner where there is one.
-  const int lo = kHalves && unit * VE >= half ? a.rot + unit * VE - half : unit * VE;
-  const int hi = kHalves && unit * VE < half ? lo + half : -1;
-  float c[NP], s[NP];
-#pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int j = kHalves ? unit * VE + k : unit * (VE / 2) + k;
-    if (j < half) {
-      const double at = j >= a.first[1] ? pos[2] : (j >= a.first[0] ? pos[1] : pos[0]);
-      const double turn = at * a.turns[j];
-      sincospif((float)(2.0 * (turn - rint(turn))), &s[k], &c[k]);
-      s[k] *= a.sign;
-    } else {
-      c[k] = 1.f;
-      s[k] = 0.f;
-    }
-  }
-  const int turned = kHalves ? (hi >= 0 ? VE : 0) : (half - unit * (VE / 2));   // pairs of the unit that turn
-  const int h0 = (int)blockIdx.y * a.chunk;
-  const int total = a.heads[0] + a.heads[1];
-  const int h1 = h0 + a.chunk < total ? h0 + a.chunk : total;
-#pragma unroll 4
-  for (int hh = h0; hh < h1; ++hh) {
-    const int which = hh >= a.heads[0] ? 1 : 0;
-    const int h = hh - (which ? a.heads[0] : 0), H = a.heads[which];
-    const int64_t dense = ((item * H + h) * a.N + tok) * a.d;
-    const T* in = static_cast<const T*>(a.in[which]) + (a.layout ? token * a.ld_in[which] + (int64_t)h * a.d : dense);
-    T* out = static_cast<T*>(a.out[which]) + (a.layout ? token * a.ld_out[which] + (int64_t)h * a.d : dense);
-    if constexpr (kHalves) {
-      Pack<T, VE> x, y;
-      x.load(in + lo);
-      if (hi >= 0) {
-        y.load(in + hi);
-        Pack<T, VE> u, v;
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          u.set(k, x.get(k) * c[k] - y.get(k) * s[k]);
-          v.set(k, x.get(k) * s[k] + y.get(k) * c[k]);
-        }
-        u.store(out + lo);
-        v.store(out + hi);
-      } else {
-        x.store(out + lo);
-      }
-    } else {
-      Pack<T, VE> x, u;
-      x.load(in + lo);
-#pragma unroll
-      for (int k = 0; k < VE / 2; ++k) {
-        if (k < turned) {
-          u.set(2 * k, x.get(2 * k) * c[k] - x.get(2 * k + 1) * s[k]);
-          u.set(2 * k + 1, x.get(2 * k) * s[k] + x.get(2 * k + 1) * c[k]);
-        } else {   // copied as they are, not multiplied by (1, 0)
-          u.e[2 * k] = x.e[2 * k];
-          u.e[2 * k + 1] = x.e[2 * k + 1];
-        }
-      }
-      u.store(out + lo);
-    }
-  }
+  const double turn = pos * a.turns[j];
+  float s, c;
+  sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+  return make_float2(c, s * a.sign);
 }
 
-// Neighbouring pairs at any alignment: one pair (or the last channel of an
-// odd d) a thread, element by element.
-template <typename T>
-__global__ void __launch_bounds__(256) rope_pair_kernel(const __grid_constant__ RopeArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= a.threads) return;
-  const int64_t token = id / a.units;
-  const int j = (int)(id - token * a.units);
-  const int64_t item = token / a.N, tok = token - item * a.N;
-  float c = 1.f, s = 0.f;
-  const bool turned = j < a.rot / 2;
-  if (turned) {
-    const int axis = j >= a.first[1] ? 2 : (j >= a.first[0] ? 1 : 0);
-    double pos;
-    if (a.positions) {
-      pos = (double)a.positions[token * 3 + axis];
-    } else {
-      const int64_t row = tok / a.width, t = row / a.height;
-      pos = a.pos0[axis] + a.step[axis] * (double)(axis == 0 ? t : (axis == 1 ? row - t * a.height : tok - row * a.width));
-    }
-    const double turn = pos * a.turns[j];
-    sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
-    s *= a.sign;
+// The unit of a thread in each head it takes.
+//   kHalves: pair j is channels (j, j + rot / 2); a unit is VE of the first and
+//   their partners, or VE channels behind the turned ones.
+//   Else: pair j is channels (2 j, 2 j + 1); a unit is VE neighbours, or (kPair)
+//   one pair loaded as single elements, or the last channel of an odd d.
+template <typename T, int VE, bool kHalves, bool kPair>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int NP = kHalves ? VE : (kPair ? 1 : VE / 2);   // pairs of a unit
+  constexpr int kLoad = kPair ? 1 : VE;                      // elements of a load
+  // Heads on their way, 64 bytes of a thread's loads: with 32 the turned heads wait
+  // (768p: 224 us against 218), with 128 registers cost occupancy (234 us).
+  constexpr int kAhead = kHalves || kPair ? 2 : 4;
+  extern __shared__ float2 table[];   // [tile][rot / 2]
+  const int half = a.rot / 2;
+  const uint32_t token0 = blockIdx.x * (uint32_t)a.tile;
+  // Neighbouring threads: the units of a head, then the lanes' heads, then the tokens.
+  const int c0 = (int)threadIdx.x / a.units, unit = (int)threadIdx.x - c0 * a.units;
+  const int local = c0 / a.lanes, lane = c0 - local * a.lanes;
+  const uint32_t token = token0 + local;
+  const bool live = local < a.tile && token < a.tokens;
+  // Channels of the unit's two loads (the second: the partner, if any).
+  int lo, hi = -1;
+  if constexpr (kHalves) {
+    lo = unit * VE < half ? unit * VE : a.rot + unit * VE - half;
+    if (unit * VE < half) hi = lo + half;
+  } else {
+    lo = unit * (kPair ? 2 : VE);
+    if (kPair && lo + 1 < a.d) hi = lo + 1;
   }
-  const bool two = 2 * j + 1 < a.d;
-  const int h0 = (int)blockIdx.y * a.chunk;
-  const int total = a.heads[0] + a.heads[1];
-  const int h1 = h0 + a.chunk < total ? h0 + a.chunk : total;
-#pragma unroll 4
-  for (int hh = h0; hh < h1; ++hh) {
-    const int which = hh >= a.heads[0] ? 1 : 0;
-    const int h = hh - (which ? a.heads[0] : 0), H = a.heads[which];
-    const int64_t dense = ((item * H + h) * a.N + tok) * a.d;
-    const T* in = static_cast<const T*>(a.in[which]) + (a.layout ? token * a.ld_in[which] + (int64_t)h * a.d : dense);
-    T* out = static_cast<T*>(a.out[which]) + (a.layout ? token * a.ld_out[which] + (int64_t)h * a.d : dense);
-    const T x = in[2 * j];
-    const T y = two ? in[2 * j + 1] : x;
-    if (turned) {
-      out[2 * j] = from_f32<T>(to_f32(x) * c - to_f32(y) * s);
-      out[2 * j + 1] = from_f32<T>(to_f32(x) * s + to_f32(y) * c);
-    } else {
-      out[2 * j] = x;
-      if (two) out[2 * j + 1] = y;
+  // Element offset of the token in head 0, and from head to head.
+  int64_t at_in[2], at_out[2], next;
+  if (a.layout) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      at_in[i] = (int64_t)token * a.ld_in[i] + lo;
+      at_out[i] = (int64_t)token * a.ld_out[i] + lo;
+    }
+    next = a.d;
+  } else {
+    const int64_t item = token / a.N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) at_in[i] = at_out[i] = (item * (a.heads[i] - 1) * a.N + token) * a.d + lo;
+    next = (int64_t)a.N * a.d;
+  }
+  const int total = live ? a.heads[0] + a.heads[1] : 0, step = hi - lo;
+  auto input = [&](int h) {
+    return h < a.heads[0] ? static_cast<const T*>(a.in[0]) + at_in[0] + h * next
+                          : static_cast<const T*>(a.in[1]) + at_in[1] + (h - a.heads[0]) * next;
+  };
+  auto output = [&](int h) {
+    return h < a.heads[0] ? static_cast<T*>(a.out[0]) + at_out[0] + h * next
+                          : static_cast<T*>(a.out[1]) + at_out[1] + (h - a.heads[0]) * next;
+  };
+  constexpr bool kTwo = kHalves || kPair;
+  Pack<T, kLoad> x[kAhead], y[kTwo ? kAhead : 1];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * a.lanes;
+      if (h < total) {
+        const T* p = input(h);
+        x[i].load(p);
+        if constexpr (kTwo) {
+          if (hi >= 0) y[i].load(p + step);
+        }
+      }
+    }
+  };
+  load(lane);
+  for (int e = threadIdx.x; e < a.tile * half; e += 256) {
+    const int tl = e / half;
+    if (token0 + tl < a.tokens) table[e] = turn_of(a, token0 + tl, e - tl * half);
+  }
+  __syncthreads();
+  const int first_pair = kHalves ? unit * VE : lo / 2;
+  const int turned = kHalves ? (hi >= 0 ? VE : 0) : half - first_pair;   // pairs of the unit that turn
+  float2 cs[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) cs[k] = live && k < turned ? table[local * half + first_pair + k] : make_float2(1.f, 0.f);
+  for (int h0 = lane; h0 < total; h0 += kAhead * a.lanes) {
+    Pack<T, kLoad> u[kAhead], v[kTwo ? kAhead : 1];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if constexpr (kTwo) {
+        u[i] = x[i];
+        v[i] = y[i];
+        if (turned > 0) {
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            u[i].set(k, x[i].get(k) * cs[k].x - y[i].get(k) * cs[k].y);
+            v[i].set(k, x[i].get(k) * cs[k].y + y[i].get(k) * cs[k].x);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          if (k < turned) {
+            const float p = x[i].get(2 * k), q = x[i].get(2 * k + 1);
+            u[i].set2(2 * k, make_float2(p * cs[k].x - q * cs[k].y, p * cs[k].y + q * cs[k].x));
+          } else {   // copied as they are, not multiplied by (1, 0)
+            u[i].e[2 * k] = x[i].e[2 * k];
+            u[i].e[2 * k + 1] = x[i].e[2 * k + 1];
+          }
+        }
+      }
+    }
+    load(h0 + kAhead * a.lanes);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * a.lanes;
+      if (h < total) {
+        T* p = output(h);
+        u[i].store(p);
+        if constexpr (kTwo) {
+          if (hi >= 0) v[i].store(p + step);
+        }
+      }
     }
   }
 }
 
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Launch: threads along x, and along y as many slices of the heads as it
-// takes to give every SM work where there are few tokens.
+// Tokens of a CTA, and threads that share a unit: four, so that the CTA reads
+// and writes 1 KB of a token at a time (768p: 218 us; 226 with two, 235 with
+// one; with eight 213, but a sequence of 8192 tokens 23 us against 20), and
+// more where there would be fewer than two CTAs for an SM (one frame of 1008
+// tokens: 7 us; with eight CTAs for an SM small clips pay for the CTAs, 5.1 us
+// against 3.4).
 template <typename Kernel>
-cudaError_t launch(Kernel k, RopeArgs& a, int64_t tokens, int units, cudaStream_t st) {
+cudaError_t launch(Kernel k, RopeArgs& a, int units, cudaStream_t st) {
   a.units = units;
-  a.threads = tokens * units;
-  const int64_t bx = (a.threads + 255) / 256;
-  const int total = a.heads[0] + a.heads[1];
-  int chunk = total;
-  while (chunk > 1 && bx * ((total + chunk - 1) / chunk) < 148 * 8) chunk = (chunk + 1) / 2;
-  a.chunk = chunk;
-  k<<<dim3((unsigned)bx, (unsigned)((total + chunk - 1) / chunk)), 256, 0, st>>>(a);
+  a.tile = 256 / (units * 4);
+  if (a.tile < 1) a.tile = 1;
+  while (a.tile > 1 && (a.tokens + a.tile - 1) / a.tile < 148 * 2) a.tile = (a.tile + 1) / 2;
+  a.lanes = 256 / (a.tile * units);
+  const uint32_t grid = (a.tokens + a.tile - 1) / a.tile;
+  k<<<grid, 256, (size_t)a.tile * (a.rot / 2) * sizeof(float2), st>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t run(RopeArgs& a, int64_t tokens, int pairing, cudaStream_t st) {
+cudaError_t run(RopeArgs& a, int pairing, cudaStream_t st) {
   const int ve = 16 / (int)sizeof(T);
   // The widest vector that every row start, stride and the width allow.
   auto fits = [&](int n) {
@@ -212,15 +223,15 @@ cudaError_t run(RopeArgs& a, int64_t tokens, int pairing, cudaStream_t st) {
   if (pairing == VDA_ROPE_HALVES) {
     auto units = [&](int n) { return a.rot / 2 / n + (a.d - a.rot) / n; };
     if constexpr (sizeof(T) == 2) {
-      if (fits(8)) return launch(rope_kernel<T, 8, true>, a, tokens, units(8), st);
+      if (fits(8)) return launch(rope_kernel<T, 8, true, false>, a, units(8), st);
     }
-    if (fits(4)) return launch(rope_kernel<T, 4, true>, a, tokens, units(4), st);
-    if (fits(2)) return launch(rope_kernel<T, 2, true>, a, tokens, units(2), st);
-    return launch(rope_kernel<T, 1, true>, a, tokens, units(1), st);
+    if (fits(4)) return launch(rope_kernel<T, 4, true, false>, a, units(4), st);
+    if (fits(2)) return launch(rope_kernel<T, 2, true, false>, a, units(2), st);
+    return launch(rope_kernel<T, 1, true, false>, a, units(1), st);
   }
-  if (fits(ve)) return launch(rope_kernel<T, 16 / (int)sizeof(T), false>, a, tokens, a.d / ve, st);
-  if (fits(2)) return launch(rope_kernel<T, 2, false>, a, tokens, a.d / 2, st);
-  return launch(rope_pair_kernel<T>, a, tokens, (a.d + 1) / 2, st);
+  if (fits(ve)) return launch(rope_kernel<T, 16 / (int)sizeof(T), false, false>, a, a.d / ve, st);
+  if (fits(2)) return launch(rope_kernel<T, 2, false, false>, a, a.d / 2, st);
+  return launch(rope_kernel<T, 2, false, true>, a, (a.d + 1) / 2, st);
 }
 
 }  // namespace
@@ -228,9 +239,9 @@ cudaError_t run(RopeArgs& a, int64_t tokens, int pairing, cudaStream_t st) {
 cudaError_t launch_rope(const vda_rope_problem& p, const void* Q, const void* K, const float* positions, void* Qo,
                         void* Ko, bool backward, cudaStream_t st) {
   RopeArgs a{};
-  a.N = (int64_t)p.T * p.height * p.width;
-  const int64_t tokens = p.B * a.N;
-  if (tokens == 0 || p.H_q + p.H_k == 0) return cudaSuccess;
+  a.N = (uint32_t)((int64_t)p.T * p.height * p.width);   // B N is below 2^31
+  a.tokens = (uint32_t)p.B * a.N;
+  if (a.tokens == 0 || p.H_q + p.H_k == 0) return cudaSuccess;
   a.in[0] = Q;
   a.in[1] = K;
   a.out[0] = Qo;
@@ -259,8 +270,8 @@ cudaError_t launch_rope(const vda_rope_problem& p, const void* Q, const void* K,
     a.pos0[ax] = p.pos0[ax];
     a.step[ax] = p.step[ax];
   }
-  return p.dtype == VDA_DTYPE_BF16 ? run<__nv_bfloat16>(a, tokens, p.pairing, st)
-                                   : run<float>(a, tokens, p.pairing, st);
+  return p.dtype == VDA_DTYPE_BF16 ? run<__nv_bfloat16>(a, p.pairing, st)
+                                   : run<float>(a, p.pairing, st);
 }
 
 }  // namespace vda
