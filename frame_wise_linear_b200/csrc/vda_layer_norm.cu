@@ -138,14 +138,60 @@ struct Pairs {
   __device__ __forceinline__ float get(int e) const { return e % 2 ? p[e / 2].y : p[e / 2].x; }
 };
 
+// The columns of w (or `none`) that a thread holds; 16 bytes at a time where a
+// vector's columns start at a multiple of that.
 template <int VE, int NV, bool kFull>
 __device__ __forceinline__ void load_columns(const void* w, const NormArgs& a, const Place<VE, NV, kFull>& p,
                                              float none, Pairs<NV * VE>& out) {
+  const bool aligned = VE >= 4 && w && ((uintptr_t)w & 15) == 0;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
+  for (int k = 0; k < NV; ++k) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-      out.set(k * VE + i, w && p.has(k) ? load_w(w, p.vec(k) * VE + i, a.w_bf16) : none);
+    for (int i = 0; i < VE; ++i) out.set(k * VE + i, none);
+    if (!w || !p.has(k)) continue;
+    if constexpr (VE >= 4) {
+      if (aligned) {
+        if (a.w_bf16) {
+          Pack<__nv_bfloat16, VE> q;
+          q.load(static_cast<const __nv_bfloat16*>(w) + p.vec(k) * VE);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) out.set(k * VE + i, q.get(i));
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; j += 4) {
+            Pack<float, 4> q;
+            q.load(static_cast<const float*>(w) + p.vec(k) * VE + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out.set(k * VE + j + i, q.get(i));
+          }
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) out.set(k * VE + i, load_w(w, p.vec(k) * VE + i, a.w_bf16));
+  }
+}
+
+// The columns of a thread to a row of sums in global or shared memory (16-byte
+// aligned where VE is 4 or 8).
+template <int VE, int NV, bool kFull>
+__device__ __forceinline__ void store_columns(float* to, const Place<VE, NV, kFull>& p, const Pairs<NV * VE>& v) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    if (!p.has(k)) continue;
+    if constexpr (VE >= 4) {
+#pragma unroll
+      for (int j = 0; j < VE; j += 4) {
+        const int e = (k * VE + j) / 2;
+        *reinterpret_cast<float4*>(to + p.vec(k) * VE + j) =
+            make_float4(v.p[e].x, v.p[e].y, v.p[e + 1].x, v.p[e + 1].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) to[p.vec(k) * VE + i] = v.get(k * VE + i);
+    }
+  }
 }
 
 // Where the threads of a CTA find the elements of a batch: kRows rows of every
@@ -512,16 +558,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
     __syncthreads();   // every thread has read its last rows
     out = fold + p.group * 2 * a.D;
   }
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (p.has(k)) {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        out[p.vec(k) * VE + i] = dw.get(k * VE + i);
-        out[a.D + p.vec(k) * VE + i] = db.get(k * VE + i);
-      }
-    }
-  }
+  store_columns(out, p, dw);
+  store_columns(out + a.D, p, db);
   if (p.groups > 1) {
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.D; c += blockDim.x) {
