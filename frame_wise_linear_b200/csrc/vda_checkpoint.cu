@@ -92,14 +92,15 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* codes, const
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     const Unit<VE> u(r, u0 + j * 256);
-    float x[VE];
-    decode_pack<VE>(c[j], scale_of(s[j]), x);
+    float2 x[VE > 1 ? VE / 2 : 1];
+    decode_pairs<VE>(c[j], x);
+    const float2 scale = both(scale_of(s[j]));
     Pack<T, VE> q;
     if constexpr (VE > 1) {
 #pragma unroll
-      for (int i = 0; i < VE; i += 2) q.set2(i, make_float2(x[i], x[i + 1]));
+      for (int i = 0; i < VE; i += 2) q.set2(i, mul2(x[i / 2], scale));
     } else {
-      q.set(0, x[0]);
+      q.set(0, x[0].x * scale.x);
     }
     if (u.in) q.store(X + u.at);
   }

@@ -399,17 +399,23 @@ __device__ __forceinline__ void load_scales(const NormArgs& a, int64_t row, int 
     if (p.has(k)) sb[k] = a.scales[row * nblk + p.vec(k) / (kBlock / VE)];
 }
 
-// All of a thread's elements of a row of codes, scaled.
+// All of a thread's elements of a row of codes, each vector's times its scale
+// times `by`.
 template <int VE, int NV, int kRows, bool kAsync, bool kFull>
 __device__ __forceinline__ void get_codes(const Batch<uint8_t, VE, NV, kRows, kAsync>& in, int buf, int r,
                                           const uint8_t* row, const Place<VE, NV, kFull>& p, const int (&sb)[NV],
-                                          Pairs<NV * VE>& out) {
+                                          float by, Pairs<NV * VE>& out) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    float x[VE];
-    decode_pack<VE>(in.get(buf, r, k, row, p), scale_of(sb[k]), x);
+    const float2 scale = both(scale_of(sb[k]) * by);
+    float2 x[VE > 1 ? VE / 2 : 1];
+    decode_pairs<VE>(in.get(buf, r, k, row, p), x);
+    if constexpr (VE > 1) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) out.set(k * VE + i, x[i]);
+      for (int j = 0; j < VE / 2; ++j) out.p[k * VE / 2 + j] = mul2(x[j], scale);
+    } else {
+      out.set(k, x[0].x * scale.x);
+    }
   }
 }
 
@@ -450,11 +456,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
       }
     }
   };
-  // The thread's dy, and xh, of row r.
-  auto get = [&](int buf, int r, int64_t row, Pairs<N>& dy, Pairs<N>& xh) {
+  // The thread's dy, and xh (of codes: times `by`), of row r.
+  auto get = [&](int buf, int r, int64_t row, float by, Pairs<N>& dy, Pairs<N>& xh) {
     iny.get(buf, r, dY + row_at(a, row, a.ld_y), p, dy);
     if constexpr (kCodes) {
-      get_codes(inx, buf, r, X + x_at(row), p, sb[r], xh);
+      get_codes(inx, buf, r, X + x_at(row), p, sb[r], by, xh);
     } else {
       inx.get(buf, r, X + x_at(row), p, xh);
 #pragma unroll
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
       float2 s1 = both(0.f), s2 = both(0.f);
       if (kWhole || row < a.rows) {
         Pairs<N> dy, xh;
-        get(buf, r, row, dy, xh);
+        get(buf, r, row, 1.f, dy, xh);
         // Where the thread has no vector dy is 0: nothing is added.
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
@@ -519,9 +525,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
       T* dx = static_cast<T*>(a.Y) + row_at(a, row, a.ld_x);
       const float2 c1 = both(-s[r] * a.inv_d), c2 = both(-s[kRows + r] * a.inv_d), rs = both(rstd[r]);
       Pairs<N> dy, xh;
-      get(buf, r, row, dy, xh);
+      get(buf, r, row, c2.x, dy, xh);
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) xh.p[j] = mul2(rs, fma2(dy.p[j], w.p[j], fma2(xh.p[j], c2, c1)));
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 t = kCodes ? add2(xh.p[j], c1) : fma2(xh.p[j], c2, c1);
+        xh.p[j] = mul2(rs, fma2(dy.p[j], w.p[j], t));
+      }
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         Pack<T, VE> d;
@@ -637,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_apply_kernel(
       if (row >= a.rows) break;
       T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
       Pairs<N> x;
-      get_codes(in, buf, r, a.codes + row * a.D, p, sb[r], x);
+      get_codes(in, buf, r, a.codes + row * a.D, p, sb[r], 1.f, x);
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) x.p[j] = fma2(x.p[j], w.p[j], b.p[j]);
 #pragma unroll

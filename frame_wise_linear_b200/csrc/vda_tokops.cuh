@@ -167,22 +167,30 @@ __device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, 
     for (int i = 0; i < VE; i += 2)
       two[i / 2] = encode2_any(make_float2(x[i], VE > 1 ? x[i + 1] : 0.f), inv_scale_of(s), s);
   }
-#pragma unroll
-  for (int i = 0; i < VE; ++i) codes.e[i] = (uint8_t)(two[i / 2] >> (8 * (i % 2)));
+  if constexpr (VE == 1) codes.e[0] = (uint8_t)two[0];
+  if constexpr (VE == 4) codes.raw = two[0] | two[1] << 16;
+  if constexpr (VE == 8) codes.raw = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
   return s;
 }
 
-// The values of VE neighbouring codes at one scale.
+// The values of VE neighbouring codes, unscaled (exact), in pairs; one code: in x.
 template <int VE>
-__device__ __forceinline__ void decode_pack(const Pack<uint8_t, VE>& c, float scale, float (&x)[VE]) {
+__device__ __forceinline__ void decode_pairs(const Pack<uint8_t, VE>& c, float2 (&out)[VE > 1 ? VE / 2 : 1]) {
+  static_assert(VE == 1 || VE == 4 || VE == 8, "1, 4 or 8 codes");
   if constexpr (VE == 1) {
-    x[0] = decode2(c.e[0]).x * scale;
+    out[0] = decode2(c.e[0]);
   } else {
+    uint32_t w[VE / 4];
+    if constexpr (VE == 4) {
+      w[0] = c.raw;
+    } else {
+      w[0] = c.raw.x;
+      w[1] = c.raw.y;
+    }
 #pragma unroll
-    for (int i = 0; i < VE; i += 2) {
-      const float2 v = mul2(decode2(c.e[i] | (uint32_t)c.e[i + 1] << 8), both(scale));
-      x[i] = v.x;
-      x[i + 1] = v.y;
+    for (int i = 0; i < VE / 4; ++i) {
+      out[2 * i] = decode2(w[i] & 0xffffu);
+      out[2 * i + 1] = decode2(w[i] >> 16);
     }
   }
 }
