@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* X, const Rows r, uin
 #pragma unroll
     for (int i = 0; i < VE; ++i) x[i] = q[j].get(i);
     Pack<uint8_t, VE> c;
-    const int s = encode_block<VE>(x, c);
+    const int s = encode_block<VE, false>(x, c, 0xffffffffu);
     if (u.in) {
       c.store(codes + u.code);
       if (threadIdx.x % (kBlock / VE) == 0) scales[u.scale] = (uint8_t)s;

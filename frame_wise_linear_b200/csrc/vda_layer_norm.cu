@@ -243,7 +243,7 @@ struct Batch {
 // 205).
 constexpr int ctas_of(int per) { return per == 32 ? 1 : 2; }
 
-template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull>
+template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull, bool kCodes>
 __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(const NormArgs a) {
   constexpr int N = NV * VE;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -360,13 +360,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
           q.set(0, y.get(k));
         }
         if (p.has(k)) q.store(yr + p.vec(k) * VE);
-        if (a.codes) {
+        if constexpr (kCodes) {
           // A thread without this vector adds nothing to the block's maximum.
+          // |xh| is at most sqrt(D) (or NaN).
           float xh[VE];
 #pragma unroll
           for (int i = 0; i < VE; ++i) xh[i] = p.has(k) ? x.get(k * VE + i) : 0.f;
           Pack<uint8_t, VE> c;
-          const int sb = encode_block<VE>(xh, c);
+          const int sb = encode_block<VE, true>(xh, c, kWhole ? 0xffffffffu : lane_group<kBlock / VE>());
           if (p.has(k)) {
             c.store(a.codes + row * a.D + p.vec(k) * VE);
             if (p.vec(k) % (kBlock / VE) == 0) a.scales[row * nblk + p.vec(k) / (kBlock / VE)] = (uint8_t)sb;
@@ -719,8 +720,9 @@ cudaError_t run_rows(Pass pass, const NormArgs& a, const Shape& s, cudaStream_t 
   constexpr bool kX = VE * sizeof(T) >= 4, kC = VE >= 4, kBoth = kX && kC;   // what cp.async can fetch
   const int grid = grid_for(a.rows, s, kRows);
   if (pass == kForward)
-    return launch(norm_fwd_kernel<T, VE, NV, kRows, kX, kFull>, grid, s.threads, Batch<T, VE, NV, kRows, kX>::kBytes, a,
-                  st);
+    return launch(a.codes ? norm_fwd_kernel<T, VE, NV, kRows, kX, kFull, true>
+                          : norm_fwd_kernel<T, VE, NV, kRows, kX, kFull, false>,
+                  grid, s.threads, Batch<T, VE, NV, kRows, kX>::kBytes, a, st);
   if (pass == kApply)
     return launch(norm_apply_kernel<T, VE, NV, kRows, kC, kFull>, grid, s.threads,
                   Batch<uint8_t, VE, NV, kRows, kC>::kBytes, a, st);

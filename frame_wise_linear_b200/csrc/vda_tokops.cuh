@@ -129,13 +129,16 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The largest of v over groups of Lanes neighbouring lanes (a power of two up
-// to 32); the lanes of a group take part together.
+// The lanes of a group of Lanes neighbours (a power of two up to 32).
 template <int Lanes>
-__device__ __forceinline__ float lanes_max(float v) {
-  const uint32_t group = (uint32_t)((1ull << Lanes) - 1) << ((threadIdx.x & 31) / Lanes * Lanes);
+__device__ __forceinline__ uint32_t lane_group() {
+  return (uint32_t)((1ull << Lanes) - 1) << ((threadIdx.x & 31) / Lanes * Lanes);
+}
+// The largest of v over a group; `mask`: lanes that are here together, whole groups.
+template <int Lanes>
+__device__ __forceinline__ float lanes_max(float v, uint32_t mask) {
 #pragma unroll
-  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(group, v, o));
+  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
   return v;
 }
 
@@ -143,17 +146,19 @@ __device__ __forceinline__ float lanes_max(float v) {
 constexpr float kLargeTop = 448.f * 0x1p119f;
 
 // VE values to codes, and the block's scale byte, by the 32 / VE neighbouring
-// lanes that hold the block (values beyond the row are 0).  fmaxf passes over
-// NaN, so a block without infinities needs no test of its elements.
-template <int VE>
-__device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, VE>& codes) {
+// lanes that hold the block (values beyond the row are 0; `mask`: the lanes that
+// are here together).  fmaxf passes over NaN, so a block without infinities
+// needs no test of its elements; kSmall: there are none, nor values near
+// float32's end.
+template <int VE, bool kSmall>
+__device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, VE>& codes, uint32_t mask) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < VE; ++i) top = fmaxf(top, fabsf(x[i]));
-  top = lanes_max<kBlock / VE>(top);
+  top = lanes_max<kBlock / VE>(top, mask);
   int s = scale_byte(top);
   uint32_t two[VE > 1 ? VE / 2 : 1];
-  if (top <= kLargeTop) {
+  if (kSmall || top <= kLargeTop) {
     const float2 inv = both(inv_scale_of(s));
 #pragma unroll
     for (int i = 0; i < VE; i += 2) two[i / 2] = encode2(mul2(make_float2(x[i], VE > 1 ? x[i + 1] : 0.f), inv));
@@ -161,7 +166,7 @@ __device__ __forceinline__ int encode_block(const float (&x)[VE], Pack<uint8_t, 
     top = 0.f;
 #pragma unroll
     for (int i = 0; i < VE; ++i) top = fmaxf(top, block_mag(x[i]));
-    top = lanes_max<kBlock / VE>(top);
+    top = lanes_max<kBlock / VE>(top, lane_group<kBlock / VE>());
     s = scale_byte(top);
 #pragma unroll
     for (int i = 0; i < VE; i += 2)
