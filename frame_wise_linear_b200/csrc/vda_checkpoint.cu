@@ -3,9 +3,12 @@
 // format), and back.
 //
 // Both directions are one pass over the data, bound by HBM: element size + 1
-// + 1/32 bytes an element.  Eight neighbouring lanes (float32) or four (bf16)
-// hold a block, 16 bytes each, and find its largest magnitude by shuffles; a
-// row that is not 16-byte aligned takes one element a lane, a warp a block.
+// + 1/32 bytes an element.  Three forms, by alignment alone:
+//   - rows of 16-byte vectors: eight neighbouring lanes (float32) or four (bf16)
+//     hold a block, 16 bytes each, and find its largest magnitude by shuffles;
+//   - dense rows at any alignment (odd widths): a CTA's blocks are one stretch of
+//     memory, copied through shared memory 16 bytes at a time on both sides;
+//   - rows with gaps at any alignment: one element a lane, a warp a block.
 #include "vda_internal.cuh"
 #include "vda_tokops.cuh"
 
@@ -22,6 +25,7 @@ struct Rows {
   uint64_t by;        // ceil(2^64 / per_row) where the quotient by it is exact, else 0
   int64_t ld;         // of the tensor
   int D, nblk;
+  int flat;           // blocks of a CTA in the any-alignment form, at most kFlat
   int whole;          // codes and tensor are dense and D is whole blocks: unit u is elements u VE ..
 };
 
@@ -106,6 +110,152 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* codes, const
   }
 }
 
+// ---- dense rows at any alignment
+constexpr int kFlat = 256;                 // blocks of a CTA, at most
+constexpr int kStretch = kFlat * kBlock;   // their elements
+
+// The elements of blocks b0 .. b0 + count - 1: neighbours in memory, from
+// element `first` on; block i starts `offs[i]` elements behind it, and
+// offs[count] is their number.
+struct Stretch {
+  int64_t first;
+  int count;
+};
+__device__ __forceinline__ Stretch stretch_of(const Rows& r, int64_t rows, int* offs) {
+  const int64_t b0 = (int64_t)blockIdx.x * r.flat, row0 = b0 / r.nblk;
+  const int col0 = (int)(b0 - row0 * r.nblk);   // first block's place in its row
+  const int64_t left = rows * r.nblk - b0;
+  const int count = left < r.flat ? (int)left : r.flat;
+  for (int i = threadIdx.x; i <= count; i += 256) {
+    const int n = col0 + i, row = n / r.nblk, col = n - row * r.nblk;
+    offs[i] = row * r.D + (col - col0) * kBlock;   // below kStretch: full blocks, or short ones
+  }
+  return Stretch{row0 * r.D + (int64_t)col0 * kBlock, count};
+}
+
+// n elements between global memory at `g` and shared memory, where element j
+// is at byte (g & 15) + j sizeof(T): 16 bytes at a time, single elements where
+// a vector at either end holds others too.
+template <typename T>
+__device__ __forceinline__ void stretch_in(const T* g, int n, uint8_t* shared) {
+  const int shift = (int)((uintptr_t)g & 15), bytes = shift + n * (int)sizeof(T);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(g) - shift;
+  for (int v = threadIdx.x * 16; v < bytes; v += 256 * 16) {
+    if (v >= shift && v + 16 <= bytes) {
+      async_copy<16>(shared + v, base + v);
+    } else {
+      const int end = v + 16 < bytes ? v + 16 : bytes;
+      for (int b = v < shift ? shift : v; b < end; b += (int)sizeof(T))
+        *reinterpret_cast<T*>(shared + b) = *reinterpret_cast<const T*>(base + b);
+    }
+  }
+  async_commit();
+  async_wait<0>();
+}
+template <typename T>
+__device__ __forceinline__ void stretch_out(T* g, int n, const uint8_t* shared) {
+  const int shift = (int)((uintptr_t)g & 15), bytes = shift + n * (int)sizeof(T);
+  uint8_t* base = reinterpret_cast<uint8_t*>(g) - shift;
+  for (int v = threadIdx.x * 16; v < bytes; v += 256 * 16) {
+    if (v >= shift && v + 16 <= bytes) {
+      *reinterpret_cast<uint4*>(base + v) = *reinterpret_cast<const uint4*>(shared + v);
+    } else {
+      const int end = v + 16 < bytes ? v + 16 : bytes;
+      for (int b = v < shift ? shift : v; b < end; b += (int)sizeof(T))
+        *reinterpret_cast<T*>(base + b) = *reinterpret_cast<const T*>(shared + b);
+    }
+  }
+}
+
+// A block is eight neighbouring lanes', four elements each; lane q of group
+// `sub` takes elements q + 8 ((m + sub) & 3), m < 4, so that the four groups of
+// a warp read different banks.
+__device__ __forceinline__ int element_of(int lane, int m) { return (lane & 7) + 8 * ((m + (lane >> 3)) & 3); }
+
+template <typename T>
+__global__ void __launch_bounds__(256) pack_flat_kernel(const T* X, const Rows r, int64_t rows, uint8_t* codes,
+                                                        uint8_t* scales) {
+  __shared__ __align__(16) uint8_t in[kStretch * sizeof(T) + 16], out[kStretch + 16];
+  __shared__ int offs[kFlat + 1];
+  __shared__ uint8_t sb[kFlat];
+  const Stretch st = stretch_of(r, rows, offs);
+  __syncthreads();
+  const int n = offs[st.count];
+  stretch_in(X + st.first, n, in);
+  __syncthreads();
+  const T* x = reinterpret_cast<const T*>(in + ((uintptr_t)(X + st.first) & 15));
+  uint8_t* c = out + ((uintptr_t)(codes + st.first) & 15);
+  const int lane = threadIdx.x & 31;
+  for (int i0 = threadIdx.x >> 5 << 2; i0 < st.count; i0 += 32) {
+    const int i = i0 + (lane >> 3);
+    const int at = offs[i < st.count ? i : st.count], size = i < st.count ? offs[i + 1] - at : 0;
+    float v[4];   // zeros behind the row's end
+    float top = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int e = element_of(lane, m);
+      v[m] = e < size ? to_f32(x[at + e]) : 0.f;
+      top = fmaxf(top, fabsf(v[m]));
+    }
+    top = lanes_max<8>(top, 0xffffffffu);
+    int s = scale_byte(top);
+    uint32_t two[2];
+    if (top <= kLargeTop) {
+      const float2 inv = both(inv_scale_of(s));
+      two[0] = encode2(mul2(make_float2(v[0], v[1]), inv));
+      two[1] = encode2(mul2(make_float2(v[2], v[3]), inv));
+    } else {
+      top = fmaxf(fmaxf(block_mag(v[0]), block_mag(v[1])), fmaxf(block_mag(v[2]), block_mag(v[3])));
+      top = lanes_max<8>(top, lane_group<8>());
+      s = scale_byte(top);
+      two[0] = encode2_any(make_float2(v[0], v[1]), inv_scale_of(s), s);
+      two[1] = encode2_any(make_float2(v[2], v[3]), inv_scale_of(s), s);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int e = element_of(lane, m);
+      if (e < size) c[at + e] = (uint8_t)(two[m / 2] >> (8 * (m % 2)));
+    }
+    if ((lane & 7) == 0 && i < st.count) sb[i] = (uint8_t)s;
+  }
+  __syncthreads();
+  stretch_out(codes + st.first, n, out);
+  if ((int)threadIdx.x < st.count) scales[(int64_t)blockIdx.x * r.flat + threadIdx.x] = sb[threadIdx.x];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) unpack_flat_kernel(const uint8_t* codes, const uint8_t* scales, const Rows r,
+                                                          int64_t rows, T* X) {
+  __shared__ __align__(16) uint8_t out[kStretch * sizeof(T) + 16], in[kStretch + 16];
+  __shared__ int offs[kFlat + 1];
+  __shared__ uint8_t sb[kFlat];
+  const Stretch st = stretch_of(r, rows, offs);
+  if ((int)threadIdx.x < st.count) sb[threadIdx.x] = scales[(int64_t)blockIdx.x * r.flat + threadIdx.x];
+  __syncthreads();
+  const int n = offs[st.count];
+  stretch_in(codes + st.first, n, in);
+  __syncthreads();
+  T* x = reinterpret_cast<T*>(out + ((uintptr_t)(X + st.first) & 15));
+  const uint8_t* c = in + ((uintptr_t)(codes + st.first) & 15);
+  const int lane = threadIdx.x & 31;
+  for (int i0 = threadIdx.x >> 5 << 2; i0 < st.count; i0 += 32) {
+    const int i = i0 + (lane >> 3);
+    if (i >= st.count) break;
+    const int at = offs[i], size = offs[i + 1] - at;
+    const float2 scale = both(scale_of(sb[i]));
+#pragma unroll
+    for (int m = 0; m < 4; m += 2) {
+      const int e0 = element_of(lane, m), e1 = element_of(lane, m + 1);
+      const uint32_t c0 = e0 < size ? c[at + e0] : 0, c1 = e1 < size ? c[at + e1] : 0;
+      const float2 v = mul2(decode2(c0 | c1 << 8), scale);
+      if (e0 < size) x[at + e0] = from_f32<T>(v.x);
+      if (e1 < size) x[at + e1] = from_f32<T>(v.y);
+    }
+  }
+  __syncthreads();
+  stretch_out(X + st.first, n, out);
+}
+
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 template <typename T>
@@ -130,10 +280,24 @@ Rows rows_for(const vda_checkpoint_problem& p, int64_t ld, int ve) {
 // CTAs of 256 threads: below 2^31, as there are fewer than 2^36 blocks of at most 32 units.
 unsigned grid_for(const Rows& r) { return (unsigned)((r.units + 256 * kUnits - 1) / (256 * kUnits)); }
 
+// Blocks of a CTA: 256, or fewer, down to the 32 that eight warps take at once,
+// until there are two CTAs for an SM (257 x 1001 float32: 8.6 us with 256).
+unsigned flat_grid(const vda_checkpoint_problem& p, Rows& r) {
+  const int64_t blocks = p.rows * r.nblk;
+  r.flat = kFlat;
+  while (r.flat > 32 && blocks < 148LL * 2 * r.flat) r.flat /= 2;
+  return (unsigned)((blocks + r.flat - 1) / r.flat);
+}
+
 template <typename T, int VE>
 cudaError_t pack(const vda_checkpoint_problem& p, const void* X, uint8_t* codes, uint8_t* scales, int64_t ld,
                  cudaStream_t st) {
-  const Rows r = rows_for(p, ld, VE);
+  Rows r = rows_for(p, ld, VE);
+  if (VE == 1 && ld == p.D) {
+    const unsigned grid = flat_grid(p, r);
+    pack_flat_kernel<T><<<grid, 256, 0, st>>>(static_cast<const T*>(X), r, p.rows, codes, scales);
+    return cudaGetLastError();
+  }
   pack_kernel<T, VE><<<grid_for(r), 256, 0, st>>>(static_cast<const T*>(X), r, codes, scales);
   return cudaGetLastError();
 }
@@ -141,7 +305,12 @@ cudaError_t pack(const vda_checkpoint_problem& p, const void* X, uint8_t* codes,
 template <typename T, int VE>
 cudaError_t unpack(const vda_checkpoint_problem& p, const uint8_t* codes, const uint8_t* scales, void* X, int64_t ld,
                    cudaStream_t st) {
-  const Rows r = rows_for(p, ld, VE);
+  Rows r = rows_for(p, ld, VE);
+  if (VE == 1 && ld == p.D) {
+    const unsigned grid = flat_grid(p, r);
+    unpack_flat_kernel<T><<<grid, 256, 0, st>>>(codes, scales, r, p.rows, static_cast<T*>(X));
+    return cudaGetLastError();
+  }
   unpack_kernel<T, VE><<<grid_for(r), 256, 0, st>>>(codes, scales, r, static_cast<T*>(X));
   return cudaGetLastError();
 }
