@@ -54,6 +54,7 @@ struct NormArgs {
   int64_t rows, ld_x, ld_y;   // ld_x: X (and dX); ld_y: Y, dY; from one token to the next
   uint64_t by_heads;   // ceil(2^64 / heads), or 0: every row is a token
   int heads, D, tpr;
+  int shift, kinds;    // rows of any width: where row 0 starts in a vector, and after how many rows that repeats
   float eps, inv_d;
   int w_bf16;
 };
@@ -92,40 +93,77 @@ __device__ __forceinline__ float half_warp_sum(float v) {
 
 constexpr int kThreads = 256;   // of a CTA at most, and the ring's stride
 
+// Which of the vectors of VE elements that a row's threads may hold it has.
+//   kAll: rows are vectors, and every thread has all of its NV.
+//   kSome: rows are vectors, and some threads have fewer.
+//   kShift: dense rows of any width.  A row starts `shift` elements into an
+//   aligned vector, and the shift repeats every `kinds` rows; a CTA takes rows
+//   of one kind, so that its threads keep their columns.  The first and last
+//   vector of a row hold elements of its neighbours, too: read and left alone.
+enum Fill { kAll, kSome, kShift };
+
 // What a thread is in its CTA, and which columns it holds: vectors t + k tpr,
-// k < NV, of VE elements; kFull: every thread has all of them.
-template <int VE, int NV, bool kFull>
+// k < NV; vector v is columns v VE - shift .. + VE - 1.
+template <int VE, int NV, int F>
 struct Place {
-  int t, group, groups, tpr, nvec, lanes, warps, lane, warp, first;
+  int t, group, groups, tpr, nvec, lanes, warps, lane, warp, first, D, shift, kind, kinds;
+  int64_t rows, cta, ctas;   // rows of this CTA's kind, its place among the CTAs that share them
   __device__ __forceinline__ explicit Place(const NormArgs& a) {
     tpr = a.tpr;
     t = (int)threadIdx.x % a.tpr;
     group = (int)threadIdx.x / a.tpr;
     groups = (int)blockDim.x / a.tpr;
-    nvec = a.D / VE;
+    D = a.D;
+    if constexpr (F == kShift) {
+      kinds = a.kinds;
+      kind = blockIdx.x % kinds;
+      cta = blockIdx.x / kinds;
+      ctas = gridDim.x / kinds;
+      rows = (a.rows - kind + kinds - 1) / kinds;
+      shift = (a.shift + kind * a.D) % VE;
+    } else {
+      kinds = 1;
+      kind = shift = 0;
+      cta = blockIdx.x;
+      ctas = gridDim.x;
+      rows = a.rows;
+    }
+    nvec = (a.D + shift + VE - 1) / VE;
     lanes = a.tpr < 32 ? a.tpr : 32;
     warps = a.tpr < 32 ? 1 : a.tpr >> 5;
     lane = threadIdx.x & 31;
     warp = threadIdx.x >> 5;
     first = warp / warps * warps;   // the row's first warp
   }
+  // Row i of this kind among all rows.
+  __device__ __forceinline__ int64_t real(int64_t i) const { return F == kShift ? i * kinds + kind : i; }
   __device__ __forceinline__ int vec(int k) const { return t + k * tpr; }
-  __device__ __forceinline__ bool has(int k) const { return kFull || vec(k) < nvec; }
+  __device__ __forceinline__ int col(int k) const { return vec(k) * VE - shift; }
+  __device__ __forceinline__ bool has(int k) const { return F == kAll || vec(k) < nvec; }
+  // Element i of vector k is one of the row's; all of vector k's are.
+  __device__ __forceinline__ bool in(int k, int i) const {
+    return F == kShift ? (unsigned)(col(k) + i) < (unsigned)D : has(k);
+  }
+  __device__ __forceinline__ bool whole(int k) const {
+    return F == kShift ? col(k) >= 0 && col(k) + VE <= D : has(k);
+  }
+  // Columns of the row among n that start at column c.
+  __device__ __forceinline__ int columns(int c, int n) const {
+    const int lo = c > 0 ? c : 0, hi = c + n < D ? c + n : D;
+    return hi > lo ? hi - lo : 0;
+  }
   __device__ __forceinline__ int elements() const {
     int n = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) n += has(k) ? VE : 0;
+    for (int k = 0; k < NV; ++k) n += F == kAll ? VE : columns(col(k), VE);
     return n;
   }
   // Elements that warp i of a row holds: vectors 32 i + k tpr .. + 31.
   __device__ __forceinline__ int warp_elements(int i) const {
     int n = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int left = nvec - (i * 32 + k * tpr);
-      n += left < 0 ? 0 : (left > 32 ? 32 : left);
-    }
-    return n * VE;
+    for (int k = 0; k < NV; ++k) n += columns((i * 32 + k * tpr) * VE - shift, 32 * VE);
+    return n;
   }
 };
 
@@ -140,10 +178,10 @@ struct Pairs {
 
 // The columns of w (or `none`) that a thread holds; 16 bytes at a time where a
 // vector's columns start at a multiple of that.
-template <int VE, int NV, bool kFull>
-__device__ __forceinline__ void load_columns(const void* w, const NormArgs& a, const Place<VE, NV, kFull>& p,
+template <int VE, int NV, int F>
+__device__ __forceinline__ void load_columns(const void* w, const NormArgs& a, const Place<VE, NV, F>& p,
                                              float none, Pairs<NV * VE>& out) {
-  const bool aligned = VE >= 4 && w && ((uintptr_t)w & 15) == 0;
+  const bool aligned = VE >= 4 && F != kShift && w && ((uintptr_t)w & 15) == 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -169,18 +207,19 @@ __device__ __forceinline__ void load_columns(const void* w, const NormArgs& a, c
       }
     }
 #pragma unroll
-    for (int i = 0; i < VE; ++i) out.set(k * VE + i, load_w(w, p.vec(k) * VE + i, a.w_bf16));
+    for (int i = 0; i < VE; ++i)
+      if (p.in(k, i)) out.set(k * VE + i, load_w(w, p.col(k) + i, a.w_bf16));
   }
 }
 
 // The columns of a thread to a row of sums in global or shared memory (16-byte
-// aligned where VE is 4 or 8).
-template <int VE, int NV, bool kFull>
-__device__ __forceinline__ void store_columns(float* to, const Place<VE, NV, kFull>& p, const Pairs<NV * VE>& v) {
+// aligned where rows are vectors of 4 or 8).
+template <int VE, int NV, int F>
+__device__ __forceinline__ void store_columns(float* to, const Place<VE, NV, F>& p, const Pairs<NV * VE>& v) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     if (!p.has(k)) continue;
-    if constexpr (VE >= 4) {
+    if constexpr (VE >= 4 && F != kShift) {
 #pragma unroll
       for (int j = 0; j < VE; j += 4) {
         const int e = (k * VE + j) / 2;
@@ -189,7 +228,8 @@ __device__ __forceinline__ void store_columns(float* to, const Place<VE, NV, kFu
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) to[p.vec(k) * VE + i] = v.get(k * VE + i);
+      for (int i = 0; i < VE; ++i)
+        if (p.in(k, i)) to[p.col(k) + i] = v.get(k * VE + i);
     }
   }
 }
@@ -198,35 +238,55 @@ __device__ __forceinline__ void store_columns(float* to, const Place<VE, NV, kFu
 // row group, two batches on the SM, one being worked on and one on its way.
 // kAsync: in shared memory, [2][kRows][NV][kThreads] vectors from `base`, each
 // thread's own, filled by its own cp.async (so no barrier is needed to read
-// them).  Else (bf16 or codes that are not aligned, which cp.async cannot
-// fetch one by one) straight from global memory, the second time from the
-// caches.
+// them).  Else (single elements) straight from global memory, the second time
+// from the caches.  Rows are given by their first element.
 template <typename T, int VE, int NV, int kRows, bool kAsync>
 struct Batch {
   static constexpr int kBytes = kAsync ? 2 * kRows * NV * VE * (int)sizeof(T) * kThreads : 0;
   T* place;
-  __device__ __forceinline__ explicit Batch(void* base) { place = static_cast<T*>(base) + (int)threadIdx.x * VE; }
+  const T *begin, *end;   // the tensor, where its rows are dense
+  __device__ __forceinline__ Batch(void* base, const T* tensor, const NormArgs& a)
+      : place(static_cast<T*>(base) + (int)threadIdx.x * VE), begin(tensor), end(tensor + a.rows * a.D) {}
   __device__ __forceinline__ T* slot(int buf, int r, int k) const {
     return place + buf * (kRows * NV * kThreads * VE) + (r * NV + k) * (kThreads * VE);
   }
-  template <bool kFull>
-  __device__ __forceinline__ void fetch(int buf, int r, const T* row, const Place<VE, NV, kFull>& p) const {
+  template <int F>
+  __device__ __forceinline__ void fetch(int buf, int r, const T* row, const Place<VE, NV, F>& p) const {
     if constexpr (kAsync) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (p.has(k)) async_copy<VE * (int)sizeof(T)>(slot(buf, r, k), row + p.vec(k) * VE);
+      for (int k = 0; k < NV; ++k) {
+        if (!p.has(k)) continue;
+        const T* from = row + p.col(k);
+        if (F != kShift || p.whole(k) || (from >= begin && from + VE <= end)) {
+          async_copy<VE * (int)sizeof(T)>(slot(buf, r, k), from);
+        } else {   // the tensor's first or last vector reaches beyond it
+#pragma unroll
+          for (int i = 0; i < VE; ++i)
+            if (p.in(k, i)) slot(buf, r, k)[i] = from[i];
+        }
+      }
     }
   }
-  template <bool kFull>
-  __device__ __forceinline__ Pack<T, VE> get(int buf, int r, int k, const T* row, const Place<VE, NV, kFull>& p) const {
+  // The thread's vector k of row r, zeros where it has no element.
+  template <int F>
+  __device__ __forceinline__ Pack<T, VE> get(int buf, int r, int k, const T* row, const Place<VE, NV, F>& p) const {
     Pack<T, VE> q;
-    if constexpr (!kFull) q.zero();
-    if (p.has(k)) q.load(kAsync ? slot(buf, r, k) : row + p.vec(k) * VE);
+    if constexpr (F != kAll) q.zero();
+    if (p.has(k)) q.load(kAsync ? slot(buf, r, k) : row + p.col(k));
+    if constexpr (F == kShift) {
+      if (!p.whole(k)) {
+        Pack<T, VE> none;
+        none.zero();
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (!p.in(k, i)) q.e[i] = none.e[i];
+      }
+    }
     return q;
   }
-  // All of the thread's elements of a row, zeros where it has none.
-  template <bool kFull>
-  __device__ __forceinline__ void get(int buf, int r, const T* row, const Place<VE, NV, kFull>& p,
+  // All of the thread's elements of a row.
+  template <int F>
+  __device__ __forceinline__ void get(int buf, int r, const T* row, const Place<VE, NV, F>& p,
                                       Pairs<NV * VE>& out) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -237,31 +297,53 @@ struct Batch {
   }
 };
 
+// A thread's elements to a row, rounded to its type.
+template <typename T, int VE, int NV, int F>
+__device__ __forceinline__ void put(T* row, const Place<VE, NV, F>& p, const Pairs<NV * VE>& v) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    Pack<T, VE> q;
+    if constexpr (VE > 1) {
+#pragma unroll
+      for (int i = 0; i < VE; i += 2) q.set2(i, v.p[(k * VE + i) / 2]);
+    } else {
+      q.set(0, v.get(k));
+    }
+    if (p.whole(k)) {
+      q.store(row + p.col(k));
+    } else if constexpr (F == kShift) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+        if (p.in(k, i)) row[p.col(k) + i] = q.e[i];
+    }
+  }
+}
+
 // CTAs of an SM that the kernels are compiled for, by the elements a thread
 // holds (two: up to 128 registers a thread; with three the rows of a batch
 // spill: 45360 x 4096 bf16 forward 190 us against 148, backward 234 against
 // 205).
 constexpr int ctas_of(int per) { return per == 32 ? 1 : 2; }
 
-template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull, bool kCodes>
+template <typename T, int VE, int NV, int kRows, bool kAsync, int F, bool kCodes>
 __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(const NormArgs a) {
   constexpr int N = NV * VE;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][kRows][kThreads / 32];   // (mean, squares) of each warp's part of a row
-  const Place<VE, NV, kFull> p(a);
+  const Place<VE, NV, F> p(a);
   const int nblk = (a.D + kBlock - 1) / kBlock;
-  const Batch<T, VE, NV, kRows, kAsync> in(ring);
   const T* X = static_cast<const T*>(a.X);
+  const Batch<T, VE, NV, kRows, kAsync> in(ring, X, a);
   // Row r of a batch that starts at row0: row0 + r groups + group.
-  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
   auto fetch = [&](int buf, int64_t row0, auto whole) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (decltype(whole)::value || row < a.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (decltype(whole)::value || at < p.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
     }
   };
-  int64_t row0 = blockIdx.x * span;
+  int64_t row0 = p.cta * span;
   fetch(0, row0, std::false_type());
   async_commit();
   Pairs<N> w, b;
@@ -269,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
   load_columns(a.bias, a, p, 0.f, b);
   const int n_t = p.elements();
   const float count_t = (float)n_t, inv_t = 1.f / (float)(n_t > 1 ? n_t : 1);
-  const float inv_w = p.warps > 1 ? 1.f / (float)p.warp_elements(p.warp - p.first) : a.inv_d;
+  const int n_w = p.warps > 1 ? p.warp_elements(p.warp - p.first) : a.D;
+  const float inv_w = n_w > 0 ? 1.f / (float)n_w : 0.f;
   // In the exchange lanes 0 - 15 and 16 - 31 look at one warp each of two rows.
   const int peer = p.lane & 15;
   const bool in_row = peer < p.warps;
@@ -279,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
     float mean[kRows], rstd[kRows], s[kRows], m2[kRows], own[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
       s[r] = m2[r] = own[r] = 0.f;
-      if (kWhole || row < a.rows) {
+      if (kWhole || at < p.rows) {
         Pairs<N> x;
         in.get(buf, r, X + row_at(a, row, a.ld_x), p, x);
         float2 sum = x.p[0];
@@ -293,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
           float2 d = add2(x.p[j], both(-own[r]));
-          if constexpr (!kFull) {
-            if (!p.has(2 * j / VE)) d.x = 0.f;
-            if (!p.has((2 * j + 1) / VE)) d.y = 0.f;
+          if constexpr (F != kAll) {
+            if (!p.in(2 * j / VE, 2 * j % VE)) d.x = 0.f;
+            if (!p.in((2 * j + 1) / VE, (2 * j + 1) % VE)) d.y = 0.f;
           }
           sq = fma2(d, d, sq);
         }
@@ -307,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
     for (int r = 0; r < kRows; ++r) {
       mean[r] = s[r] * inv_w;
       const float d = own[r] - mean[r];
-      m2[r] += kFull || n_t > 0 ? count_t * d * d : 0.f;
+      m2[r] += F == kAll || n_t > 0 ? count_t * d * d : 0.f;
     }
     lanes_sum(m2, p.lanes);
     if (p.warps > 1) {
@@ -339,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (!kWhole && row >= a.rows) break;
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (!kWhole && at >= p.rows) break;
       const T* xr = X + row_at(a, row, a.ld_x);
       T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
       Pairs<N> x, y;
@@ -350,17 +433,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
         x.p[j] = mul2(add2(x.p[j], both(-mean[r])), both(rstd[r]));
         y.p[j] = fma2(x.p[j], w.p[j], b.p[j]);
       }
+      put(yr, p, y);
+      if constexpr (kCodes) {
+        static_assert(F != kShift, "a block's lanes are those of one vector of four or eight");
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        Pack<T, VE> q;
-        if constexpr (VE > 1) {
-#pragma unroll
-          for (int i = 0; i < VE; i += 2) q.set2(i, y.p[(k * VE + i) / 2]);
-        } else {
-          q.set(0, y.get(k));
-        }
-        if (p.has(k)) q.store(yr + p.vec(k) * VE);
-        if constexpr (kCodes) {
+        for (int k = 0; k < NV; ++k) {
           // A thread without this vector adds nothing to the block's maximum.
           // |xh| is at most sqrt(D) (or NaN).
           float xh[VE];
@@ -380,42 +457,58 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
       }
     }
   };
-  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
-    if (row0 + step + span <= a.rows) fetch(buf ^ 1, row0 + step, std::true_type());
+  for (int buf = 0; row0 < p.rows; row0 += step, buf ^= 1) {
+    if (row0 + step + span <= p.rows) fetch(buf ^ 1, row0 + step, std::true_type());
     else fetch(buf ^ 1, row0 + step, std::false_type());
     async_commit();
     async_wait<1>();
     // All but a batch that the rows' end cuts off need no test of each row.
-    if (row0 + span <= a.rows) body(buf, row0, std::true_type());
+    if (row0 + span <= p.rows) body(buf, row0, std::true_type());
     else body(buf, row0, std::false_type());
   }
 }
 
-// The scale bytes of a thread's vectors of a row.
-template <int VE, int NV, bool kFull>
-__device__ __forceinline__ void load_scales(const NormArgs& a, int64_t row, int nblk, const Place<VE, NV, kFull>& p,
+// The scale bytes of a thread's vectors of a row; a shifted vector may reach
+// from one block into the next, whose byte is then the second.
+template <int VE, int NV, int F>
+__device__ __forceinline__ void load_scales(const NormArgs& a, int64_t row, int nblk, const Place<VE, NV, F>& p,
                                             int (&sb)[NV]) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (p.has(k)) sb[k] = a.scales[row * nblk + p.vec(k) / (kBlock / VE)];
+  for (int k = 0; k < NV; ++k) {
+    if (!p.has(k)) continue;
+    if constexpr (F == kShift) {
+      const int lo = p.col(k) > 0 ? p.col(k) : 0, hi = p.col(k) + VE <= a.D ? p.col(k) + VE - 1 : a.D - 1;
+      sb[k] = a.scales[row * nblk + lo / kBlock] | a.scales[row * nblk + hi / kBlock] << 8;
+    } else {
+      sb[k] = a.scales[row * nblk + p.vec(k) / (kBlock / VE)];
+    }
+  }
 }
 
-// All of a thread's elements of a row of codes, each vector's times its scale
+// All of a thread's elements of a row of codes, each times its block's scale
 // times `by`.
-template <int VE, int NV, int kRows, bool kAsync, bool kFull>
+template <int VE, int NV, int kRows, bool kAsync, int F>
 __device__ __forceinline__ void get_codes(const Batch<uint8_t, VE, NV, kRows, kAsync>& in, int buf, int r,
-                                          const uint8_t* row, const Place<VE, NV, kFull>& p, const int (&sb)[NV],
+                                          const uint8_t* row, const Place<VE, NV, F>& p, const int (&sb)[NV],
                                           float by, Pairs<NV * VE>& out) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const float2 scale = both(scale_of(sb[k]) * by);
+    const float scale = scale_of(sb[k] & 255) * by;
     float2 x[VE > 1 ? VE / 2 : 1];
     decode_pairs<VE>(in.get(buf, r, k, row, p), x);
-    if constexpr (VE > 1) {
+    if constexpr (F == kShift) {
+      // Elements up to the end of the first one's block.
+      const int split = kBlock - (p.col(k) > 0 ? p.col(k) % kBlock : p.col(k));
+      const float next = scale_of(sb[k] >> 8) * by;
 #pragma unroll
-      for (int j = 0; j < VE / 2; ++j) out.p[k * VE / 2 + j] = mul2(x[j], scale);
+      for (int j = 0; j < VE / 2; ++j)
+        out.p[k * VE / 2 + j] =
+            mul2(x[j], make_float2(2 * j < split ? scale : next, 2 * j + 1 < split ? scale : next));
+    } else if constexpr (VE > 1) {
+#pragma unroll
+      for (int j = 0; j < VE / 2; ++j) out.p[k * VE / 2 + j] = mul2(x[j], both(scale));
     } else {
-      out.set(k, x[0].x * scale.x);
+      out.set(k, x[0].x * scale);
     }
   }
 }
@@ -424,7 +517,7 @@ __device__ __forceinline__ void get_codes(const Batch<uint8_t, VE, NV, kRows, kA
 // with rstd.  Writes dX, and with a.partial the CTA's sums of dy xh and dy.
 // A batch's elements are read twice from shared memory, for the sums and for
 // dX: kept in registers they would cost 32 a row, and the occupancy with them.
-template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull, bool kCodes>
+template <typename T, int VE, int NV, int kRows, bool kAsync, int F, bool kCodes>
 __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(const NormArgs a) {
   constexpr int N = NV * VE, kSb = kCodes ? NV : 1;
   using U = typename std::conditional<kCodes, uint8_t, T>::type;   // what xh comes from
@@ -432,23 +525,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
   using InX = Batch<U, VE, NV, kRows, kAsync>;
   extern __shared__ __align__(16) uint8_t ring[];   // afterwards: groups > 1: [groups][2 D] partial sums
   __shared__ float red[2][2 * kRows][kThreads / 32];
-  const Place<VE, NV, kFull> p(a);
+  const Place<VE, NV, F> p(a);
   const int nblk = (a.D + kBlock - 1) / kBlock;
-  const InY iny(ring);
-  const InX inx(ring + InY::kBytes);
   const T* dY = static_cast<const T*>(a.dY);
   const U* X = kCodes ? reinterpret_cast<const U*>(a.codes) : static_cast<const U*>(a.X);
+  const InY iny(ring, dY, a);
+  const InX inx(ring + InY::kBytes, X, a);
   auto x_at = [&](int64_t row) { return kCodes ? row * a.D : row_at(a, row, a.ld_x); };
   // rstd, and mean or the scale bytes, of the batch that is worked on and of
   // the next: loaded with it, so that they too are there when it is.
   float mean[kRows], rstd[kRows], next_mean[kRows], next_rstd[kRows];
   int sb[kRows][kSb], next_sb[kRows][kSb];
-  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
   auto fetch = [&](int buf, int64_t row0, auto whole) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (decltype(whole)::value || row < a.rows) {
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (decltype(whole)::value || at < p.rows) {
         iny.fetch(buf, r, dY + row_at(a, row, a.ld_y), p);
         inx.fetch(buf, r, X + x_at(row), p);
         next_rstd[r] = a.rstd[row];
@@ -474,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
 #pragma unroll
     for (int k = 0; k < kSb; ++k) next_sb[r][k] = 0;
   }
-  int64_t row0 = blockIdx.x * span;
+  int64_t row0 = p.cta * span;
   fetch(0, row0, std::false_type());
   async_commit();
   Pairs<N> w, dw, db;
@@ -486,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
     float s[2 * kRows];   // of g, then of g xh
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
       float2 s1 = both(0.f), s2 = both(0.f);
-      if (kWhole || row < a.rows) {
+      if (kWhole || at < p.rows) {
         Pairs<N> dy, xh;
         get(buf, r, row, 1.f, dy, xh);
         // Where the thread has no vector dy is 0: nothing is added.
@@ -521,8 +614,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (!kWhole && row >= a.rows) break;
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (!kWhole && at >= p.rows) break;
       T* dx = static_cast<T*>(a.Y) + row_at(a, row, a.ld_x);
       const float2 c1 = both(-s[r] * a.inv_d), c2 = both(-s[kRows + r] * a.inv_d), rs = both(rstd[r]);
       Pairs<N> dy, xh;
@@ -532,20 +625,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
         const float2 t = kCodes ? add2(xh.p[j], c1) : fma2(xh.p[j], c2, c1);
         xh.p[j] = mul2(rs, fma2(dy.p[j], w.p[j], t));
       }
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        Pack<T, VE> d;
-        if constexpr (VE > 1) {
-#pragma unroll
-          for (int i = 0; i < VE; i += 2) d.set2(i, xh.p[(k * VE + i) / 2]);
-        } else {
-          d.set(0, xh.get(k));
-        }
-        if (p.has(k)) d.store(dx + p.vec(k) * VE);
-      }
+      put(dx, p, xh);
     }
   };
-  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+  for (int buf = 0; row0 < p.rows; row0 += step, buf ^= 1) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       mean[r] = next_mean[r];
@@ -553,11 +636,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
 #pragma unroll
       for (int k = 0; k < kSb; ++k) sb[r][k] = next_sb[r][k];
     }
-    if (row0 + step + span <= a.rows) fetch(buf ^ 1, row0 + step, std::true_type());
+    if (row0 + step + span <= p.rows) fetch(buf ^ 1, row0 + step, std::true_type());
     else fetch(buf ^ 1, row0 + step, std::false_type());
     async_commit();
     async_wait<1>();
-    if (row0 + span <= a.rows) body(buf, row0, std::true_type());
+    if (row0 + span <= p.rows) body(buf, row0, std::true_type());
     else body(buf, row0, std::false_type());
   }
   if (!a.partial) return;
@@ -581,8 +664,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
 }
 
 // dW and db from the CTAs' partial sums [parts][2 D]: 32 columns a block,
-// thread (x, y) adds rows y, y + 32, ...; then a warp the 32 sums of a column.  The rows come from L2; there are at most 296 of them, so a thread
-// has ten loads, all on their way at once.
+// thread (x, y) adds rows y, y + 32, ...; then a warp the 32 sums of a column.
+// The rows come from L2; there are at most 296 of them, so a thread has ten
+// loads, all on their way at once.
 __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* partial, int parts, int D, float* dW, float* db) {
   __shared__ float sh[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
@@ -608,32 +692,32 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* partial, i
 }
 
 // y = xh w + b from the 8-bit normalised rows.
-template <typename T, int VE, int NV, int kRows, bool kAsync, bool kFull>
+template <typename T, int VE, int NV, int kRows, bool kAsync, int F>
 __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_apply_kernel(const NormArgs a) {
   constexpr int N = NV * VE;
   extern __shared__ __align__(16) uint8_t ring[];
-  const Place<VE, NV, kFull> p(a);
+  const Place<VE, NV, F> p(a);
   const int nblk = (a.D + kBlock - 1) / kBlock;
-  const Batch<uint8_t, VE, NV, kRows, kAsync> in(ring);
+  const Batch<uint8_t, VE, NV, kRows, kAsync> in(ring, a.codes, a);
   int sb[kRows][NV], next_sb[kRows][NV] = {};
-  const int64_t span = (int64_t)p.groups * kRows, step = gridDim.x * span;
+  const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
   auto fetch = [&](int buf, int64_t row0) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (row < a.rows) {
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (at < p.rows) {
         in.fetch(buf, r, a.codes + row * a.D, p);
         load_scales(a, row, nblk, p, next_sb[r]);
       }
     }
   };
-  int64_t row0 = blockIdx.x * span;
+  int64_t row0 = p.cta * span;
   fetch(0, row0);
   async_commit();
   Pairs<N> w, b;
   load_columns(a.W, a, p, 1.f, w);
   load_columns(a.bias, a, p, 0.f, b);
-  for (int buf = 0; row0 < a.rows; row0 += step, buf ^= 1) {
+  for (int buf = 0; row0 < p.rows; row0 += step, buf ^= 1) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
@@ -643,20 +727,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_apply_kernel(
     async_wait<1>();
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * p.groups + p.group;
-      if (row >= a.rows) break;
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (at >= p.rows) break;
       T* yr = static_cast<T*>(a.Y) + row_at(a, row, a.ld_y);
       Pairs<N> x;
       get_codes(in, buf, r, a.codes + row * a.D, p, sb[r], 1.f, x);
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) x.p[j] = fma2(x.p[j], w.p[j], b.p[j]);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        Pack<T, VE> q;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) q.set(i, x.get(k * VE + i));
-        if (p.has(k)) q.store(yr + p.vec(k) * VE);
-      }
+      put(yr, p, x);
     }
   }
 }
@@ -669,31 +747,30 @@ bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 // takes a power of two up to 32 threads, at least the lanes of one block, or
 // whole warps.
 struct Shape {
-  int per, tpr, threads, groups;
-  bool full;
+  int per, tpr, threads, groups, kinds;
+  Fill fill;
 };
-Shape shape_for(int D, int ve) {
-  const int least = kBlock / ve, nvec = D / ve;
-  const int per = D <= 8 * least ? 8 : (D <= 16 * kThreads ? 16 : 32);
+Shape shape_for(int D, int ve, int kinds = 0) {
+  const int least = kBlock / ve, nvec = kinds ? (D + 2 * ve - 2) / ve : D / ve;   // kinds: at any shift
+  const int per = nvec * ve <= 8 * least ? 8 : (nvec * ve <= 16 * kThreads ? 16 : 32);
   const int need = (nvec + per / ve - 1) / (per / ve);
   int tpr = least;
   while (tpr < 32 && tpr < need) tpr *= 2;
   if (need > 32) tpr = (need + 31) / 32 * 32;
-  const int groups = kThreads / tpr;
-  return Shape{per, tpr, tpr * groups, groups, nvec == tpr * (per / ve)};
+  const int groups = tpr > kThreads ? 0 : kThreads / tpr;   // 0: more than the CTA's threads
+  return Shape{per,    tpr, tpr * groups, groups, kinds ? kinds : 1, kinds ? kShift
+                                                                     : nvec == tpr * (per / ve) ? kAll : kSome};
 }
 
 // CTAs for `rows` rows in batches of `n` rows a group: as many as are resident
-// at once, or as there are batches.
+// at once, or as there are batches; as many for each kind.
 int grid_for(int64_t rows, const Shape& s, int n) {
-  const int64_t batches = (rows + (int64_t)s.groups * n - 1) / ((int64_t)s.groups * n);
-  const int64_t most = 148 * ctas_of(s.per);
-  return (int)(batches < most ? batches : most);
+  const int64_t each = (rows + s.kinds - 1) / s.kinds, batches = (each + (int64_t)s.groups * n - 1) / ((int64_t)s.groups * n);
+  const int64_t most = 148 * ctas_of(s.per) / s.kinds;
+  return (int)(batches < most ? batches : most) * s.kinds;
 }
 // Batches of several rows where every CTA gets one all the same.
-bool batched(int64_t rows, const Shape& s, int n) {
-  return rows >= (int64_t)grid_for(rows, s, 1) * s.groups * n;
-}
+bool batched(int64_t rows, const Shape& s, int n) { return rows >= (int64_t)grid_for(rows, s, 1) * s.groups * n; }
 
 // 16-byte vectors where the width, the strides and the pointers allow them.
 template <typename T>
@@ -701,6 +778,25 @@ bool wide(const NormArgs& a) {
   const int ve = 16 / (int)sizeof(T);
   return a.D % ve == 0 && a.ld_x % ve == 0 && a.ld_y % ve == 0 && aligned_to(a.X, 16) && aligned_to(a.dY, 16) &&
          aligned_to(a.Y, 16) && aligned_to(a.codes, ve);
+}
+
+// Rows of any width by vectors: dense tensors that start at the same place of a
+// vector.  Rows narrower than four vectors would leave most of a vector unused.
+template <typename T>
+bool shifted(const NormArgs& a) {
+  const int ve = 16 / (int)sizeof(T);
+  if (a.D < 4 * ve || a.ld_x != a.D || a.ld_y != a.D || a.heads != 1) return false;
+  const int place = (int)((uintptr_t)a.Y / sizeof(T) % ve);
+  auto same = [&](const void* x) { return !x || (int)((uintptr_t)x / sizeof(T) % ve) == place; };
+  return same(a.X) && same(a.dY) && (!a.codes || (int)((uintptr_t)a.codes % ve) == place) &&
+         shape_for(a.D, ve, 1).groups > 0;
+}
+// After how many rows of D elements the place in a vector repeats, or the rows
+// there are.
+int kinds_for(int D, int ve, int64_t rows) {
+  int n = 1;
+  while (n * D % ve) n *= 2;
+  return rows < n ? (int)rows : n;
 }
 
 template <typename Kernel>
@@ -715,24 +811,27 @@ cudaError_t launch(Kernel k, int grid, int threads, int sh, const NormArgs& a, c
 
 enum Pass { kForward, kBackward, kApply };
 
-template <typename T, int VE, int NV, int kRows, bool kFull>
+template <typename T, int VE, int NV, int kRows, int F>
 cudaError_t run_rows(Pass pass, const NormArgs& a, const Shape& s, cudaStream_t st) {
-  constexpr bool kX = VE * sizeof(T) >= 4, kC = VE >= 4, kBoth = kX && kC;   // what cp.async can fetch
+  constexpr bool kX = VE > 1, kC = VE > 1, kBoth = kX && kC;
   const int grid = grid_for(a.rows, s, kRows);
-  if (pass == kForward)
-    return launch(a.codes ? norm_fwd_kernel<T, VE, NV, kRows, kX, kFull, true>
-                          : norm_fwd_kernel<T, VE, NV, kRows, kX, kFull, false>,
-                  grid, s.threads, Batch<T, VE, NV, kRows, kX>::kBytes, a, st);
+  if (pass == kForward) {
+    auto k = norm_fwd_kernel<T, VE, NV, kRows, kX, F, false>;
+    if constexpr (F != kShift) {
+      if (a.codes) k = norm_fwd_kernel<T, VE, NV, kRows, kX, F, true>;
+    }
+    return launch(k, grid, s.threads, Batch<T, VE, NV, kRows, kX>::kBytes, a, st);
+  }
   if (pass == kApply)
-    return launch(norm_apply_kernel<T, VE, NV, kRows, kC, kFull>, grid, s.threads,
+    return launch(norm_apply_kernel<T, VE, NV, kRows, kC, F>, grid, s.threads,
                   Batch<uint8_t, VE, NV, kRows, kC>::kBytes, a, st);
   const int fold = a.partial && s.groups > 1 ? s.groups * 2 * a.D * (int)sizeof(float) : 0;
   if (a.codes) {
     const int sh = Batch<T, VE, NV, kRows, kBoth>::kBytes + Batch<uint8_t, VE, NV, kRows, kBoth>::kBytes;
-    return launch(norm_bwd_kernel<T, VE, NV, kRows, kBoth, kFull, true>, grid, s.threads, sh > fold ? sh : fold, a, st);
+    return launch(norm_bwd_kernel<T, VE, NV, kRows, kBoth, F, true>, grid, s.threads, sh > fold ? sh : fold, a, st);
   }
   const int sh = 2 * Batch<T, VE, NV, kRows, kX>::kBytes;
-  return launch(norm_bwd_kernel<T, VE, NV, kRows, kX, kFull, false>, grid, s.threads, sh > fold ? sh : fold, a, st);
+  return launch(norm_bwd_kernel<T, VE, NV, kRows, kX, F, false>, grid, s.threads, sh > fold ? sh : fold, a, st);
 }
 
 // Rows of a batch: 128 bytes of a thread's loads on their way, where there are
@@ -742,45 +841,57 @@ constexpr int batch_rows(int element, int per, bool backward) {
   return n < 1 ? 1 : n > 4 ? 4 : n;
 }
 
-template <typename T, int VE, int NV, bool kFull>
-cudaError_t run_shape(Pass pass, NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
-  a.tpr = s.tpr;
-  if (pass != kBackward) {
-    constexpr int n = batch_rows(sizeof(T), VE * NV, false);
-    return batched(a.rows, s, n) ? run_rows<T, VE, NV, n, kFull>(pass, a, s, st)
-                                        : run_rows<T, VE, NV, 1, kFull>(pass, a, s, st);
-  }
-  constexpr int n = batch_rows(sizeof(T), VE * NV, true);
-  const bool many = batched(a.rows, s, n);
-  cudaError_t e = many ? run_rows<T, VE, NV, n, kFull>(pass, a, s, st) : run_rows<T, VE, NV, 1, kFull>(pass, a, s, st);
+template <typename T, int VE, int NV, int F>
+cudaError_t run_shape(Pass pass, const NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
+  // Single elements: one row a batch (their loads are not ahead of their use).
+  constexpr int most = VE == 1 ? 1 : batch_rows(sizeof(T), VE * NV, false);
+  constexpr int most_backward = VE == 1 ? 1 : batch_rows(sizeof(T), VE * NV, true);
+  if (pass != kBackward)
+    return batched(a.rows, s, most) ? run_rows<T, VE, NV, most, F>(pass, a, s, st)
+                                    : run_rows<T, VE, NV, 1, F>(pass, a, s, st);
+  const bool many = batched(a.rows, s, most_backward);
+  cudaError_t e =
+      many ? run_rows<T, VE, NV, most_backward, F>(pass, a, s, st) : run_rows<T, VE, NV, 1, F>(pass, a, s, st);
   if (e != cudaSuccess || !a.partial) return e;
-  const int parts = grid_for(a.rows, s, many ? n : 1);
+  const int parts = grid_for(a.rows, s, many ? most_backward : 1);
   norm_fold_kernel<<<(2 * a.D + 31) / 32, 1024, 0, st>>>(a.partial, parts, a.D, dW, db);
   return cudaGetLastError();
 }
 
 template <typename T, int VE, int NV>
-cudaError_t run_per(Pass pass, NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
-  // Single elements are the path of odd widths: kept to one variant.
+cudaError_t run_fill(Pass pass, const NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
   if constexpr (VE > 1) {
-    if (s.full) return run_shape<T, VE, NV, true>(pass, a, s, dW, db, st);
+    if (s.fill == kAll) return run_shape<T, VE, NV, kAll>(pass, a, s, dW, db, st);
+    if (s.fill == kShift) return run_shape<T, VE, NV, kShift>(pass, a, s, dW, db, st);
   }
-  return run_shape<T, VE, NV, false>(pass, a, s, dW, db, st);
+  return run_shape<T, VE, NV, kSome>(pass, a, s, dW, db, st);   // single elements too
 }
 
 template <typename T, int VE>
-cudaError_t run_wide(Pass pass, NormArgs& a, float* dW, float* db, cudaStream_t st) {
-  const Shape s = shape_for(a.D, VE);
-  if (s.per == 8) return run_per<T, VE, 8 / VE>(pass, a, s, dW, db, st);
-  if (s.per == 16) return run_per<T, VE, 16 / VE>(pass, a, s, dW, db, st);
-  return run_per<T, VE, 32 / VE>(pass, a, s, dW, db, st);
+cudaError_t run_per(Pass pass, NormArgs& a, const Shape& s, float* dW, float* db, cudaStream_t st) {
+  a.tpr = s.tpr;
+  a.kinds = s.kinds;
+  if (s.per == 8) return run_fill<T, VE, 8 / VE>(pass, a, s, dW, db, st);
+  if (s.per == 16) return run_fill<T, VE, 16 / VE>(pass, a, s, dW, db, st);
+  return run_fill<T, VE, 32 / VE>(pass, a, s, dW, db, st);
+}
+
+template <typename T>
+cudaError_t run_type(Pass pass, NormArgs& a, float* dW, float* db, cudaStream_t st) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  if (wide<T>(a)) return run_per<T, VE>(pass, a, shape_for(a.D, VE), dW, db, st);
+  // (A block of codes that is being made needs its elements in neighbouring
+  // lanes, which shifted vectors do not give.)
+  if (shifted<T>(a) && !(pass == kForward && a.codes)) {
+    a.shift = (int)((uintptr_t)a.Y / sizeof(T) % VE);
+    return run_per<T, VE>(pass, a, shape_for(a.D, VE, kinds_for(a.D, VE, a.rows)), dW, db, st);
+  }
+  return run_per<T, 1>(pass, a, shape_for(a.D, 1), dW, db, st);
 }
 
 cudaError_t run(Pass pass, int dtype, NormArgs& a, float* dW, float* db, cudaStream_t st) {
-  using bf = __nv_bfloat16;
-  if (dtype == VDA_DTYPE_BF16)
-    return wide<bf>(a) ? run_wide<bf, 8>(pass, a, dW, db, st) : run_wide<bf, 1>(pass, a, dW, db, st);
-  return wide<float>(a) ? run_wide<float, 4>(pass, a, dW, db, st) : run_wide<float, 1>(pass, a, dW, db, st);
+  return dtype == VDA_DTYPE_BF16 ? run_type<__nv_bfloat16>(pass, a, dW, db, st)
+                                 : run_type<float>(pass, a, dW, db, st);
 }
 
 NormArgs args_for(const vda_norm_problem& p) {
@@ -810,10 +921,12 @@ size_t norm_backward_workspace_bytes(const vda_norm_problem& p) {
   const int64_t rows = p.tokens * p.heads;
   if (rows == 0) return 0;
   int parts = 0;
-  for (int ve : {1, 4, 8}) {
-    const int g = grid_for(rows, shape_for(p.D, ve), 1);
-    parts = g > parts ? g : parts;
-  }
+  for (int ve : {1, 4, 8})
+    for (int kinds : {0, ve > 1 ? kinds_for(p.D, ve, rows) : 0}) {
+      const Shape s = shape_for(p.D, ve, kinds);
+      const int g = s.groups ? grid_for(rows, s, 1) : 0;
+      parts = g > parts ? g : parts;
+    }
   return align_up((size_t)parts * 2 * p.D * sizeof(float), 256);
 }
 
