@@ -127,6 +127,8 @@ _lock = threading.Lock()
 def load(path: str | None = None):
     """Loads libvda.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -207,17 +209,27 @@ def make_problem(B, H, T, n, n_txt, d_k, d_v, dtype, lam, layout=0, test_stall=0
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream of the current device, without making a Stream object where torch offers that."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.init()
+        _raw_stream = (lambda: raw(torch._C._cuda_getDevice())) if raw else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
