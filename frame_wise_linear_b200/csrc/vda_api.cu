@@ -498,9 +498,14 @@ vda_status norm_backward_impl(const vda_norm_problem* p, const void* dY, const v
         return fail(VDA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     }
   }
-  cudaError_t e = vda::launch_layer_norm_backward(
-      *p, dY, X, mean, rstd, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), W, dX, dW, dbias,
-      static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+  float* partial = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e =
+      from_checkpoint
+          ? vda::launch_layer_norm_backward_from_checkpoint(*p, dY, static_cast<const uint8_t*>(codes),
+                                                            static_cast<const uint8_t*>(scales), rstd, W, dX, dW,
+                                                            dbias, partial, st)
+          : vda::launch_layer_norm_backward(*p, dY, X, mean, rstd, W, dX, dW, dbias, partial, st);
   if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
   return VDA_OK;
 }

@@ -160,17 +160,24 @@ bool make_tok_map(CUtensorMap* m, const void* ptr, int layout, int B, int H, int
 // box_rows rows with the 128-byte swizzle (vda_tma.cu).  False on failure.
 bool make_f32_rows_map(CUtensorMap* m, const void* ptr, long long rows, int box_rows);
 
-// Layer norm (vda_layer_norm.cu).  codes and scales null: no checkpoint
-// (forward), X and mean instead of it (backward).  `partial`: workspace of
+// Layer norm (vda_layer_norm_fwd.cu, vda_layer_norm_bwd.cu, vda_layer_norm_ckpt.cu).
+// codes and scales of the forward null: no checkpoint.  `partial`: workspace of
 // norm_backward_workspace_bytes(), used where dW or db is given.
 size_t norm_backward_workspace_bytes(const vda_norm_problem& p);
 cudaError_t launch_layer_norm(const vda_norm_problem& p, const void* X, const void* W, const void* bias, void* Y,
                               float* mean, float* rstd, uint8_t* codes, uint8_t* scales, cudaStream_t st);
 cudaError_t launch_layer_norm_backward(const vda_norm_problem& p, const void* dY, const void* X, const float* mean,
-                                       const float* rstd, const uint8_t* codes, const uint8_t* scales, const void* W,
-                                       void* dX, float* dW, float* db, float* partial, cudaStream_t st);
+                                       const float* rstd, const void* W, void* dX, float* dW, float* db,
+                                       float* partial, cudaStream_t st);
+cudaError_t launch_layer_norm_backward_from_checkpoint(const vda_norm_problem& p, const void* dY,
+                                                       const uint8_t* codes, const uint8_t* scales, const float* rstd,
+                                                       const void* W, void* dX, float* dW, float* db, float* partial,
+                                                       cudaStream_t st);
 cudaError_t launch_layer_norm_from_checkpoint(const vda_norm_problem& p, const uint8_t* codes, const uint8_t* scales,
                                               const void* W, const void* bias, void* Y, cudaStream_t st);
+// dW and db from `parts` rows of partial sums [2 D] (0 without tokens).
+cudaError_t launch_norm_fold(const vda_norm_problem& p, const float* partial, int parts, float* dW, float* db,
+                             cudaStream_t st);
 
 // Rotary positions on Q and K, or (backward) their gradients (vda_rope.cu).
 cudaError_t launch_rope(const vda_rope_problem& p, const void* Q, const void* K, const float* positions, void* Qo,

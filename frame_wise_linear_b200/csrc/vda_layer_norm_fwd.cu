@@ -1,0 +1,197 @@
+// Layer norm's forward (vda_layer_norm.cuh has the plan).
+#include "vda_layer_norm.cuh"
+
+namespace vda {
+namespace {
+
+template <typename T, int VE, int NV, int kRows, bool kAsync, int F, bool kCodes>
+__global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(const NormArgs a) {
+  constexpr int kChunks = NV / kOf<VE>, kSize = Chunk<VE>::kSize;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][kRows][kThreads / 32];   // (mean, squares) of each warp's part of a row
+  const Place<VE, NV, F> p(a);
+  const int nblk = (a.D + kBlock - 1) / kBlock;
+  const T* X = static_cast<const T*>(a.X);
+  const Batch<T, VE, NV, kRows, kAsync> in(ring, X, a);
+  // Row r of a batch that starts at row0: row0 + r groups + group.
+  const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
+  auto fetch = [&](int buf, int64_t row0, auto whole) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      if (decltype(whole)::value || at < p.rows) in.fetch(buf, r, X + row_at(a, row, a.ld_x), p);
+    }
+  };
+  int64_t row0 = p.cta * span;
+  fetch(0, row0, std::false_type());
+  async_commit();
+  Chunk<VE> w[kChunks], b[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    get_columns(a.W, a, p, c, 1.f, w[c]);
+    get_columns(a.bias, a, p, c, 0.f, b[c]);
+  }
+  const int n_t = p.elements();
+  const float count_t = (float)n_t, inv_t = 1.f / (float)(n_t > 1 ? n_t : 1);
+  const int n_w = p.warps > 1 ? p.warp_elements(p.warp - p.first) : a.D;
+  const float inv_w = n_w > 0 ? 1.f / (float)n_w : 0.f;
+  // In the exchange lanes 0 - 15 and 16 - 31 look at one warp each of two rows.
+  const int peer = p.lane & 15;
+  const bool in_row = peer < p.warps;
+  const float weight = in_row ? (float)p.warp_elements(peer) * a.inv_d : 0.f;
+  auto body = [&](int buf, int64_t row0, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    float mean[kRows], rstd[kRows], s[kRows], m2[kRows], own[kRows];
+    // One row stays in registers until it is written; of several each is read
+    // again from shared memory (kept, they spill: 144 us against 133 for
+    // 45360 x 4096 bf16).
+    constexpr bool kKeep = kRows == 1;
+    Chunk<VE> kept[kChunks];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+      s[r] = m2[r] = own[r] = 0.f;
+      if (kWhole || at < p.rows) {
+        Chunk<VE>(&x)[kChunks] = kept;
+        float2 sum = both(0.f);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          get_chunk(in, buf, r, X + row_at(a, row, a.ld_x), p, c, x[c]);
+#pragma unroll
+          for (int j = 0; j < kSize / 2; ++j) sum = add2(sum, x[c].p[j]);
+        }
+        s[r] = sum.x + sum.y;
+        own[r] = s[r] * inv_t;   // the thread's own mean
+        float2 sq = both(0.f);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int j = 0; j < kSize / 2; ++j) {
+            float2 d = add2(x[c].p[j], both(-own[r]));
+            if constexpr (F != kAll) {
+              const int e = c * kSize + 2 * j;
+              if (!p.in(e / VE, e % VE)) d.x = 0.f;
+              if (!p.in((e + 1) / VE, (e + 1) % VE)) d.y = 0.f;
+            }
+            sq = fma2(d, d, sq);
+          }
+        m2[r] = sq.x + sq.y;
+      }
+    }
+    lanes_sum(s, p.lanes);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      mean[r] = s[r] * inv_w;
+      const float d = own[r] - mean[r];
+      m2[r] += F == kAll || n_t > 0 ? count_t * d * d : 0.f;
+    }
+    lanes_sum(m2, p.lanes);
+    if (p.warps > 1) {
+      if (p.lane == 0) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) red[buf][r][p.warp] = make_float2(mean[r], m2[r]);
+      }
+      // A warp that writes this half again has passed the barrier of the batch
+      // between, as has every reader after reading.
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRows; r += 2) {
+        const int of = kRows > 1 ? r + (p.lane >> 4) : 0;
+        const float2 e = in_row ? red[buf][of][p.first + peer] : make_float2(0.f, 0.f);
+        const float m = half_warp_sum(e.x * weight);
+        const float d = e.x - m;
+        const float var = half_warp_sum(in_row ? e.y * a.inv_d + weight * d * d : 0.f);
+        const float rs = 1.f / sqrtf(var + a.eps);
+        mean[r] = __shfl_sync(0xffffffffu, m, 0);
+        rstd[r] = __shfl_sync(0xffffffffu, rs, 0);
+        if (kRows > 1) {
+          mean[r + 1 < kRows ? r + 1 : r] = __shfl_sync(0xffffffffu, m, 16);
+          rstd[r + 1 < kRows ? r + 1 : r] = __shfl_sync(0xffffffffu, rs, 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) rstd[r] = 1.f / sqrtf(m2[r] * a.inv_d + a.eps);
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+        if (!kWhole && at >= p.rows) continue;
+        Chunk<VE> x, y;
+        if constexpr (kKeep) x = kept[c];
+        else get_chunk(in, buf, r, X + row_at(a, row, a.ld_x), p, c, x);
+#pragma unroll
+        for (int j = 0; j < kSize / 2; ++j) {
+          x.p[j] = mul2(add2(x.p[j], both(-mean[r])), both(rstd[r]));
+          y.p[j] = fma2(x.p[j], w[c].p[j], b[c].p[j]);
+        }
+        put_chunk(static_cast<T*>(a.Y) + row_at(a, row, a.ld_y), p, c, y);
+        if constexpr (kCodes) {
+          static_assert(F != kShift, "a block's lanes are those of one vector of four or eight");
+#pragma unroll
+          for (int k = 0; k < kOf<VE>; ++k) {
+            // A thread without this vector adds nothing to the block's maximum.
+            // |xh| is at most sqrt(D) (or NaN).
+            const int n = c * kOf<VE> + k;
+            float xh[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) xh[i] = p.has(n) ? x.get(k * VE + i) : 0.f;
+            Pack<uint8_t, VE> q;
+            const int sb = encode_block<VE, true>(xh, q, kWhole ? 0xffffffffu : lane_group<kBlock / VE>());
+            if (p.has(n)) {
+              q.store(a.codes + row * a.D + p.vec(n) * VE);
+              if (p.vec(n) % (kBlock / VE) == 0) a.scales[row * nblk + p.vec(n) / (kBlock / VE)] = (uint8_t)sb;
+            }
+          }
+        }
+      }
+    }
+    if (p.t == 0) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
+        if (!kWhole && at >= p.rows) continue;
+        if (a.mean) a.mean[row] = mean[r];
+        if (a.rstd) a.rstd[row] = rstd[r];
+      }
+    }
+  };
+  for (int buf = 0; row0 < p.rows; row0 += step, buf ^= 1) {
+    if (row0 + step + span <= p.rows) fetch(buf ^ 1, row0 + step, std::true_type());
+    else fetch(buf ^ 1, row0 + step, std::false_type());
+    async_commit();
+    async_wait<1>();
+    // All but a batch that the rows' end cuts off need no test of each row.
+    if (row0 + span <= p.rows) body(buf, row0, std::true_type());
+    else body(buf, row0, std::false_type());
+  }
+}
+
+template <int kPass, typename T, int VE, int NV, int kRows, int F>
+cudaError_t launch_pass(const NormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+  constexpr bool kAsync = VE > 1;
+  return launch(norm_fwd_kernel<T, VE, NV, kRows, kAsync, F, kPass == kForwardCodes>, grid, s.threads,
+                Batch<T, VE, NV, kRows, kAsync>::kBytes, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm(const vda_norm_problem& p, const void* X, const void* W, const void* bias, void* Y,
+                              float* mean, float* rstd, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  NormArgs a = args_for(p);
+  if (a.rows == 0) return cudaSuccess;
+  a.X = X;
+  a.W = W;
+  a.bias = bias;
+  a.Y = Y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  int ctas = 0;
+  return codes ? run_pass<kForwardCodes>(p.dtype, a, &ctas, st) : run_pass<kForward>(p.dtype, a, &ctas, st);
+}
+
+}  // namespace vda
