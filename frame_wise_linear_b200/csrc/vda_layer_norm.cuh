@@ -280,8 +280,12 @@ __device__ __forceinline__ void get_chunk(const Batch<T, VE, NV, kRows, kAsync>&
 #pragma unroll
   for (int k = 0; k < kOf<VE>; ++k) {
     const Pack<T, VE> q = in.get(buf, r, c * kOf<VE> + k, row, p);
+    if constexpr (VE > 1) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) out.set(k * VE + i, q.get(i));
+      for (int i = 0; i < VE; i += 2) out.p[i / 2] = q.get2(i);
+    } else {
+      out.set(k, q.get(0));
+    }
   }
 }
 

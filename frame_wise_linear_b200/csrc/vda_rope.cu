@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           if (k < turned) {
-            const float p = x[i].get(2 * k), q = x[i].get(2 * k + 1);
+            const float2 v = x[i].get2(2 * k);
+            const float p = v.x, q = v.y;
             u[i].set2(2 * k, make_float2(p * cs[k].x - q * cs[k].y, p * cs[k].y + q * cs[k].x));
           } else {   // copied as they are, not multiplied by (1, 0)
             u[i].e[2 * k] = x[i].e[2 * k];

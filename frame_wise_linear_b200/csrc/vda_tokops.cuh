@@ -48,6 +48,7 @@ struct Pack {
   union {
     Raw raw;
     T e[VE];
+    uint32_t w[(VE * (int)sizeof(T) + 3) / 4];
   };
   __device__ __forceinline__ Pack() {}
   __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
@@ -55,12 +56,17 @@ struct Pack {
   __device__ __forceinline__ void zero() { raw = Raw{}; }
   __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
   __device__ __forceinline__ void set(int i, float x) { e[i] = from_f32<T>(x); }
-  // Elements i and i + 1 (i even) in one conversion.
+  // Elements i and i + 1 (i even), word by word.
+  __device__ __forceinline__ float2 get2(int i) const {
+    if constexpr (sizeof(T) == 2)
+      return make_float2(__uint_as_float(w[i / 2] << 16), __uint_as_float(w[i / 2] & 0xffff0000u));
+    else
+      return make_float2(to_f32(e[i]), to_f32(e[i + 1]));
+  }
   __device__ __forceinline__ void set2(int i, float2 v) {
     if constexpr (sizeof(T) == 2) {
       const __nv_bfloat162 b = __float22bfloat162_rn(v);
-      e[i] = b.x;
-      e[i + 1] = b.y;
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&b);
     } else {
       e[i] = from_f32<T>(v.x);
       e[i + 1] = from_f32<T>(v.y);
