@@ -289,6 +289,22 @@ __device__ __forceinline__ void get_chunk(const Batch<T, VE, NV, kRows, kAsync>&
   }
 }
 
+// The same plus `by`.
+template <typename T, int VE, int NV, int kRows, bool kAsync, int F>
+__device__ __forceinline__ void get_plus(const Batch<T, VE, NV, kRows, kAsync>& in, int buf, int r, const T* row,
+                                         const Place<VE, NV, F>& p, int c, float by, Chunk<VE>& out) {
+#pragma unroll
+  for (int k = 0; k < kOf<VE>; ++k) {
+    const Pack<T, VE> q = in.get(buf, r, c * kOf<VE> + k, row, p);
+    if constexpr (VE > 1) {
+#pragma unroll
+      for (int i = 0; i < VE; i += 2) out.p[i / 2] = plus2(q, i, both(by));
+    } else {
+      out.set(k, q.get(0) + by);
+    }
+  }
+}
+
 // Chunk c of a row, rounded to its type.
 template <typename T, int VE, int NV, int F>
 __device__ __forceinline__ void put_chunk(T* row, const Place<VE, NV, F>& p, int c, const Chunk<VE>& v) {

@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
   auto x_at = [&](int64_t row) { return kCodes ? row * a.D : row_at(a, row, a.ld_x); };
   // rstd, and mean or the scale bytes, of the batch that is worked on and of
   // the next: loaded with it, so that they too are there when it is.
-  float mean[kRows], rstd[kRows], next_mean[kRows], next_rstd[kRows];
-  int sb[kRows][kSb], next_sb[kRows][kSb];
+  float mean[kRows] = {}, rstd[kRows] = {}, next_mean[kRows] = {}, next_rstd[kRows] = {};
+  int sb[kRows][kSb] = {}, next_sb[kRows][kSb] = {};
   const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
   auto fetch = [&](int buf, int64_t row0, auto whole) {
 #pragma unroll
@@ -70,17 +70,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
     if constexpr (kCodes) {
       get_codes(inx, buf, r, X + x_at(row), p, sb[r], by, c, xh);
     } else {
-      get_chunk(inx, buf, r, X + x_at(row), p, c, xh);
+      get_plus(inx, buf, r, X + x_at(row), p, c, -mean[r], xh);
 #pragma unroll
-      for (int j = 0; j < kSize / 2; ++j) xh.p[j] = mul2(add2(xh.p[j], both(-mean[r])), both(rstd[r]));
+      for (int j = 0; j < kSize / 2; ++j) xh.p[j] = mul2(xh.p[j], both(rstd[r]));
     }
   };
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    next_mean[r] = next_rstd[r] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSb; ++k) next_sb[r][k] = 0;
-  }
   int64_t row0 = p.cta * span;
   fetch(0, row0, std::false_type());
   async_commit();

@@ -12,7 +12,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_apply_kernel(
   const Place<VE, NV, F> p(a);
   const int nblk = (a.D + kBlock - 1) / kBlock;
   const Batch<uint8_t, VE, NV, kRows, kAsync> in(ring, a.codes, a);
-  int sb[kRows][NV], next_sb[kRows][NV] = {};
+  int sb[kRows][NV] = {}, next_sb[kRows][NV] = {};
   const int64_t span = (int64_t)p.groups * kRows, step = p.ctas * span;
   auto fetch = [&](int buf, int64_t row0) {
 #pragma unroll

@@ -42,40 +42,53 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
   auto body = [&](int buf, int64_t row0, auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
     float mean[kRows], rstd[kRows], s[kRows], m2[kRows], own[kRows];
-    // One row stays in registers until it is written; of several each is read
-    // again from shared memory (kept, they spill: 144 us against 133 for
+    // One float32 row stays in registers until it is written; of several each is
+    // read again from shared memory (kept, they spill: 144 us against 133 for
     // 45360 x 4096 bf16).
-    constexpr bool kKeep = kRows == 1;
+    constexpr bool kKeep = kRows == 1 && sizeof(T) == 4;
     Chunk<VE> kept[kChunks];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
       s[r] = m2[r] = own[r] = 0.f;
       if (kWhole || at < p.rows) {
-        Chunk<VE>(&x)[kChunks] = kept;
-        float2 sum = both(0.f);
+        const T* xr = X + row_at(a, row, a.ld_x);
+        Pack<T, VE> q[NV];
+        float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          get_chunk(in, buf, r, X + row_at(a, row, a.ld_x), p, c, x[c]);
+        for (int k = 0; k < NV; ++k) {
+          q[k] = in.get(buf, r, k, xr, p);
+          if constexpr (VE > 1) {
 #pragma unroll
-          for (int j = 0; j < kSize / 2; ++j) sum = add2(sum, x[c].p[j]);
+            for (int i = 0; i < VE; i += 2) sum[i / 2 % 2] = plus2(q[k], i, sum[i / 2 % 2]);
+          } else {
+            sum[k / 2 % 2].x += q[k].get(0);
+          }
         }
-        s[r] = sum.x + sum.y;
+        sum[0] = add2(sum[0], sum[1]);
+        s[r] = sum[0].x + sum[0].y;
         own[r] = s[r] * inv_t;   // the thread's own mean
-        float2 sq = both(0.f);
+        float2 sq[2] = {both(0.f), both(0.f)};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
           for (int j = 0; j < kSize / 2; ++j) {
-            float2 d = add2(x[c].p[j], both(-own[r]));
+            const int e = c * kSize + 2 * j;   // of the thread's NV VE
+            float2 d;
+            if constexpr (VE > 1) d = plus2(q[c], 2 * j, both(-own[r]));
+            else d = make_float2(q[e].get(0) - own[r], q[e + 1].get(0) - own[r]);
+            if constexpr (kKeep) {
+              if constexpr (VE > 1) kept[c].p[j] = q[c].get2(2 * j);
+              else kept[c].p[j] = make_float2(q[e].get(0), q[e + 1].get(0));
+            }
             if constexpr (F != kAll) {
-              const int e = c * kSize + 2 * j;
               if (!p.in(e / VE, e % VE)) d.x = 0.f;
               if (!p.in((e + 1) / VE, (e + 1) % VE)) d.y = 0.f;
             }
-            sq = fma2(d, d, sq);
+            sq[j % 2] = fma2(d, d, sq[j % 2]);
           }
-        m2[r] = sq.x + sq.y;
+        sq[0] = add2(sq[0], sq[1]);
+        m2[r] = sq[0].x + sq[0].y;
       }
     }
     lanes_sum(s, p.lanes);
@@ -120,11 +133,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
         const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
         if (!kWhole && at >= p.rows) continue;
         Chunk<VE> x, y;
-        if constexpr (kKeep) x = kept[c];
-        else get_chunk(in, buf, r, X + row_at(a, row, a.ld_x), p, c, x);
+        if constexpr (kKeep) {
+#pragma unroll
+          for (int j = 0; j < kSize / 2; ++j) x.p[j] = add2(kept[c].p[j], both(-mean[r]));
+        } else {
+          get_plus(in, buf, r, X + row_at(a, row, a.ld_x), p, c, -mean[r], x);
+        }
 #pragma unroll
         for (int j = 0; j < kSize / 2; ++j) {
-          x.p[j] = mul2(add2(x.p[j], both(-mean[r])), both(rstd[r]));
+          x.p[j] = mul2(x.p[j], both(rstd[r]));
           y.p[j] = fma2(x.p[j], w[c].p[j], b[c].p[j]);
         }
         put_chunk(static_cast<T*>(a.Y) + row_at(a, row, a.ld_y), p, c, y);

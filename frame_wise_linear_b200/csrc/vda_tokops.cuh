@@ -117,6 +117,20 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// Elements i and i + 1 of a vector (i even) plus c: bf16 is added to float32 as
+// it is, without being widened first (exact operands, one rounding to float32).
+template <typename T, int VE>
+__device__ __forceinline__ float2 plus2(const Pack<T, VE>& q, int i, float2 c) {
+  if constexpr (sizeof(T) == 2) {
+    float2 r;
+    asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(r.x) : "h"((uint16_t)q.w[i / 2]), "f"(c.x));
+    asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(r.y) : "h"((uint16_t)(q.w[i / 2] >> 16)), "f"(c.y));
+    return r;
+  } else {
+    return add2(q.get2(i), c);
+  }
+}
+
 // The lanes of a group of Lanes neighbours (a power of two up to 32).
 template <int Lanes>
 __device__ __forceinline__ uint32_t lane_group() {
