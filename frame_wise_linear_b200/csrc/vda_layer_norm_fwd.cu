@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
     // read again from shared memory (kept, they spill: 144 us against 133 for
     // 45360 x 4096 bf16).
     constexpr bool kKeep = kRows == 1 && sizeof(T) == 4;
-    Chunk<VE> kept[kChunks];
+    [[maybe_unused]] Chunk<VE> kept[kChunks];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t at = row0 + r * p.groups + p.group, row = p.real(at);
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_fwd_kernel(co
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
           for (int j = 0; j < kSize / 2; ++j) {
-            const int e = c * kSize + 2 * j;   // of the thread's NV VE
+            [[maybe_unused]] const int e = c * kSize + 2 * j;   // of the thread's NV VE
             float2 d;
             if constexpr (VE > 1) d = plus2(q[c], 2 * j, both(-own[r]));
             else d = make_float2(q[e].get(0) - own[r], q[e + 1].get(0) - own[r]);

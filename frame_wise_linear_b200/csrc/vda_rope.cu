@@ -74,9 +74,11 @@ template <typename T, int VE, bool kHalves, bool kPair>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int NP = kHalves ? VE : (kPair ? 1 : VE / 2);   // pairs of a unit
   constexpr int kLoad = kPair ? 1 : VE;                      // elements of a load
-  // Heads on their way, 64 bytes of a thread's loads: with 32 the turned heads wait
-  // (768p: 224 us against 218), with 128 registers cost occupancy (234 us).
-  constexpr int kAhead = kHalves || kPair ? 2 : 4;
+  // Heads on their way: 64 bytes of a thread's loads (with 32 the turned heads
+  // wait, 768p 224 us against 218; with 128 registers cost occupancy, 234 us), at
+  // most four heads, and two where pairs are loaded element by element.
+  constexpr int kLoadBytes = (kHalves || kPair ? 2 : 1) * (kPair ? 1 : VE) * (int)sizeof(T);
+  constexpr int kAhead = kHalves && VE == 1 ? 2 : 64 / kLoadBytes < 4 ? 64 / kLoadBytes : 4;
   extern __shared__ float2 table[];   // [tile][rot / 2]
   const int half = a.rot / 2;
   const uint32_t token0 = blockIdx.x * (uint32_t)a.tile;
