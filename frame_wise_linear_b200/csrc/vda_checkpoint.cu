@@ -118,10 +118,11 @@ constexpr int kStretch = kFlat * kBlock;   // their elements
 // element `first` on; block i starts `offs[i]` elements behind it, and
 // offs[count] is their number.
 struct Stretch {
-  int64_t first;
+  int64_t first, row0;   // row0: the first block's row
   int count;
 };
-__device__ __forceinline__ Stretch stretch_of(const Rows& r, int64_t rows, int* offs) {
+// `in_row`, where given: each block's row, counted from the first one's.
+__device__ __forceinline__ Stretch stretch_of(const Rows& r, int64_t rows, int* offs, int* in_row = nullptr) {
   const int64_t b0 = (int64_t)blockIdx.x * r.flat, row0 = b0 / r.nblk;
   const int col0 = (int)(b0 - row0 * r.nblk);   // first block's place in its row
   const int64_t left = rows * r.nblk - b0;
@@ -129,8 +130,9 @@ __device__ __forceinline__ Stretch stretch_of(const Rows& r, int64_t rows, int* 
   for (int i = threadIdx.x; i <= count; i += 256) {
     const int n = col0 + i, row = n / r.nblk, col = n - row * r.nblk;
     offs[i] = row * r.D + (col - col0) * kBlock;   // below kStretch: full blocks, or short ones
+    if (in_row) in_row[i] = row;
   }
-  return Stretch{row0 * r.D + (int64_t)col0 * kBlock, count};
+  return Stretch{row0 * r.D + (int64_t)col0 * kBlock, row0, count};
 }
 
 // n elements between global memory at `g` and shared memory, where element j
@@ -172,13 +174,14 @@ __device__ __forceinline__ void stretch_out(T* g, int n, const uint8_t* shared) 
 // a warp read different banks.
 __device__ __forceinline__ int element_of(int lane, int m) { return (lane & 7) + 8 * ((m + (lane >> 3)) & 3); }
 
-template <typename T>
-__global__ void __launch_bounds__(256) pack_flat_kernel(const T* X, const Rows r, int64_t rows, uint8_t* codes,
-                                                        uint8_t* scales) {
+// kNorm: packs (x - mean) rstd, each row with its own, in place of x.
+template <typename T, bool kNorm>
+__global__ void __launch_bounds__(256) pack_flat_kernel(const T* X, const Rows r, int64_t rows, const float* mean,
+                                                        const float* rstd, uint8_t* codes, uint8_t* scales) {
   __shared__ __align__(16) uint8_t in[kStretch * sizeof(T) + 16], out[kStretch + 16];
-  __shared__ int offs[kFlat + 1];
+  __shared__ int offs[kFlat + 1], in_row[kNorm ? kFlat + 1 : 1];
   __shared__ uint8_t sb[kFlat];
-  const Stretch st = stretch_of(r, rows, offs);
+  const Stretch st = stretch_of(r, rows, offs, kNorm ? in_row : nullptr);
   __syncthreads();
   const int n = offs[st.count];
   stretch_in(X + st.first, n, in);
@@ -189,12 +192,20 @@ __global__ void __launch_bounds__(256) pack_flat_kernel(const T* X, const Rows r
   for (int i0 = threadIdx.x >> 5 << 2; i0 < st.count; i0 += 32) {
     const int i = i0 + (lane >> 3);
     const int at = offs[i < st.count ? i : st.count], size = i < st.count ? offs[i + 1] - at : 0;
+    float shift = 0.f, factor = 1.f;
+    if constexpr (kNorm) {
+      if (i < st.count) {
+        shift = -mean[st.row0 + in_row[i]];
+        factor = rstd[st.row0 + in_row[i]];
+      }
+    }
     float v[4];   // zeros behind the row's end
     float top = 0.f;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int e = element_of(lane, m);
       v[m] = e < size ? to_f32(x[at + e]) : 0.f;
+      if constexpr (kNorm) v[m] = e < size ? (v[m] + shift) * factor : 0.f;
       top = fmaxf(top, fabsf(v[m]));
     }
     top = lanes_max<8>(top, 0xffffffffu);
@@ -295,10 +306,20 @@ cudaError_t pack(const vda_checkpoint_problem& p, const void* X, uint8_t* codes,
   Rows r = rows_for(p, ld, VE);
   if (VE == 1 && ld == p.D) {
     const unsigned grid = flat_grid(p, r);
-    pack_flat_kernel<T><<<grid, 256, 0, st>>>(static_cast<const T*>(X), r, p.rows, codes, scales);
+    pack_flat_kernel<T, false><<<grid, 256, 0, st>>>(static_cast<const T*>(X), r, p.rows, nullptr, nullptr, codes,
+                                                     scales);
     return cudaGetLastError();
   }
   pack_kernel<T, VE><<<grid_for(r), 256, 0, st>>>(static_cast<const T*>(X), r, codes, scales);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pack_normalised(const vda_checkpoint_problem& p, const void* X, const float* mean, const float* rstd,
+                            uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  Rows r = rows_for(p, p.D, 1);
+  const unsigned grid = flat_grid(p, r);
+  pack_flat_kernel<T, true><<<grid, 256, 0, st>>>(static_cast<const T*>(X), r, p.rows, mean, rstd, codes, scales);
   return cudaGetLastError();
 }
 
@@ -326,6 +347,12 @@ cudaError_t launch_checkpoint_pack(const vda_checkpoint_problem& p, const void* 
                                                   : pack<__nv_bfloat16, 1>(p, X, codes, scales, ld, st);
   return wide<float>(X, codes, p.D, ld) ? pack<float, 4>(p, X, codes, scales, ld, st)
                                         : pack<float, 1>(p, X, codes, scales, ld, st);
+}
+
+cudaError_t launch_checkpoint_pack_normalised(const vda_checkpoint_problem& p, const void* X, const float* mean,
+                                              const float* rstd, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  return p.dtype == VDA_DTYPE_BF16 ? pack_normalised<__nv_bfloat16>(p, X, mean, rstd, codes, scales, st)
+                                   : pack_normalised<float>(p, X, mean, rstd, codes, scales, st);
 }
 
 cudaError_t launch_checkpoint_unpack(const vda_checkpoint_problem& p, const uint8_t* codes, const uint8_t* scales,

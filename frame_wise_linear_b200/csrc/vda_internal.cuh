@@ -186,6 +186,9 @@ cudaError_t launch_rope(const vda_rope_problem& p, const void* Q, const void* K,
 // 8-bit checkpoints (vda_checkpoint.cu).
 cudaError_t launch_checkpoint_pack(const vda_checkpoint_problem& p, const void* X, uint8_t* codes, uint8_t* scales,
                                    cudaStream_t st);
+// (x - mean) rstd of dense rows at any alignment, as a checkpoint.
+cudaError_t launch_checkpoint_pack_normalised(const vda_checkpoint_problem& p, const void* X, const float* mean,
+                                              const float* rstd, uint8_t* codes, uint8_t* scales, cudaStream_t st);
 cudaError_t launch_checkpoint_unpack(const vda_checkpoint_problem& p, const uint8_t* codes, const uint8_t* scales,
                                      void* X, cudaStream_t st);
 

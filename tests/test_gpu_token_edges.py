@@ -243,3 +243,40 @@ def test_calls_on_a_side_stream_follow_it():
     vda.vda_layer_norm(p, src, None, None, Y, stream=s)     # a stream given
     s.synchronize()
     assert torch.equal(Y, Z)
+
+
+@pytest.mark.parametrize("D", [33, 77, 1001])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_kept_rows_of_odd_widths(D, dtype):
+    """The checkpoint of an odd-width norm is that of (x - mean) rstd with the statistics the call returns, whether
+    the call writes over X, keeps its statistics, or neither: bit for bit."""
+    import torch
+    from frame_wise_linear_b200 import vda
+    n, dt = 413, dtype_of(dtype)
+    X = (torch.randn(n, D, device="cuda") + 0.5).to(dt)
+    W, b = torch.randn(2, D, device="cuda")
+    p = vda.make_norm_problem(n, D, code_of(dtype), eps=EPS)
+    nblk = -(-D // 32)
+
+    def run(x, y, stats):
+        codes = torch.full((n, D), 9, dtype=torch.uint8, device="cuda")
+        scales = torch.full((n, nblk), 9, dtype=torch.uint8, device="cuda")
+        vda.vda_layer_norm(p, x, W, b, y, *stats, codes, scales)
+        return codes, scales
+
+    mean, rstd = torch.empty(2, n, device="cuda")
+    Y = torch.empty_like(X)
+    codes, scales = run(X, Y, (mean, rstd))
+    xh = (X.float() - mean[:, None]) * rstd[:, None]
+    c, s = o.checkpoint(f64(xh))
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    # Other forms of the kernel sum in another order: their statistics, and with them a value at a border between
+    # two codes, may differ in the last place; one code step is 2^-3 of a value at most.
+    for over, stats in ((True, (torch.empty(n, device="cuda"), torch.empty(n, device="cuda"))), (False, (None, None))):
+        x = X.clone()
+        y = x if over else torch.empty_like(X)
+        codes2, scales2 = run(x, y, stats)
+        v, ref = o.checkpoint_values(codes2.cpu().numpy(), scales2.cpu().numpy()), o.checkpoint_values(c, s)
+        differ = v != ref
+        assert differ.mean() <= 1e-3
+        assert np.all(np.abs(v - ref)[differ] <= 2.0 ** -3 * np.abs(f64(xh))[differ] * (1 + 2.0 ** -4))
