@@ -1,6 +1,6 @@
 // Layer norm over the last dimension, forward and backward, optionally with
 // the normalised row kept in 8 bits for the backward: what the passes share
-// (vda_layer_norm_fwd.cu, vda_layer_norm_bwd.cu).
+// (vda_layer_norm_fwd.cu, vda_layer_norm_bwd.cu, vda_layer_norm_ckpt.cu).
 //
 //   forward    m = sum x / D, r = 1 / sqrt(sum (x - m)^2 / D + eps),
 //              xh = (x - m) r, y = xh w + b
@@ -9,14 +9,17 @@
 //
 // Both are bound by HBM: a row is read once, stays on the SM between its sums
 // and its outputs, and is written once.  A row belongs to `tpr` threads, each
-// with 16 of its elements as 16-byte vectors (single elements where rows are
-// not 16-byte aligned).  A CTA walks over batches of rows, with the next batch
+// with 16 of its elements as 16-byte vectors (Fill, below, has what is done
+// where rows are not 16-byte aligned).  A CTA walks over batches of rows, with the next batch
 // already on its way: every thread copies its own vectors into its own places
 // in shared memory (cp.async), so they need no barrier, cost no registers and
 // keep HBM busy while a batch is summed and written.  Several rows a batch
 // let the chains of their sums overlap, and share the barrier of a row's
-// warps.  Next to HBM the instructions count (a row of 4096 has 550 ns on its
-// SM in the backward), hence float32 in pairs.
+// warps.  Next to HBM the instructions count (a row of 4096 bf16 has 550 ns on
+// its SM in the backward, and the clock falls under the power cap), hence
+// float32 in pairs and bf16 added to float32 as it is.  45360 x 4096 bf16:
+// forward 118 us (0.96 of the copy rate, 0.89 in a long run), backward 188 us
+// (0.90; 0.84).
 //
 // The row's sums: shuffles within a warp, and where a row has several warps
 // one exchange through shared memory with one barrier a batch.  In the forward
@@ -43,6 +46,7 @@ namespace vda {
 namespace {   // each source file that includes this compiles its own kernels
 
 using namespace tokops;
+
 struct NormArgs {
   const void* X;       // forward: input; backward: input (or null: codes)
   const void* dY;      // backward
@@ -74,6 +78,7 @@ __device__ __forceinline__ int64_t row_at(const NormArgs& a, int64_t row, int64_
 __device__ __forceinline__ float load_w(const void* w, int i, int w_bf16) {
   return w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
 }
+
 // Sums over a group of neighbouring lanes (lanes: a power of two).
 template <int N>
 __device__ __forceinline__ void lanes_sum(float (&v)[N], int lanes) {
@@ -99,11 +104,14 @@ constexpr int kThreads = 256;   // of a CTA at most, and the ring's stride
 
 // Which of the vectors of VE elements that a row's threads may hold it has.
 //   kAll: rows are vectors, and every thread has all of its NV.
-//   kSome: rows are vectors, and some threads have fewer.
+//   kSome: rows are vectors, and some threads have fewer.  (Vectors of one
+//   element: rows with gaps at odd places, and narrow odd rows.)
 //   kShift: dense rows of any width.  A row starts `shift` elements into an
 //   aligned vector, and the shift repeats every `kinds` rows; a CTA takes rows
 //   of one kind, so that its threads keep their columns.  The first and last
 //   vector of a row hold elements of its neighbours, too: read and left alone.
+//   45360 x 1001 bf16: forward 64 us, backward 92 us; by single elements 126
+//   and 190 us.
 enum Fill { kAll, kSome, kShift };
 
 // What a thread is in its CTA, and which columns it holds: vectors t + k tpr,
@@ -180,7 +188,7 @@ struct Chunk {
   __device__ __forceinline__ void set(int e, float v) { (e % 2 ? p[e / 2].y : p[e / 2].x) = v; }
   __device__ __forceinline__ float get(int e) const { return e % 2 ? p[e / 2].y : p[e / 2].x; }
 };
-// Vectors of chunk c: k0(c) .. k0(c) + kOf - 1.
+// Vectors of a chunk: chunk c is vectors c kOf .. c kOf + kOf - 1.
 template <int VE>
 constexpr int kOf = VE > 1 ? 1 : 2;
 
@@ -395,14 +403,15 @@ Shape shape_for(int D, int ve, int kinds = 0) {
   while (tpr < 32 && tpr < need) tpr *= 2;
   if (need > 32) tpr = (need + 31) / 32 * 32;
   const int groups = tpr > kThreads ? 0 : kThreads / tpr;   // 0: more than the CTA's threads
-  return Shape{per,    tpr, tpr * groups, groups, kinds ? kinds : 1, kinds ? kShift
-                                                                     : nvec == tpr * (per / ve) ? kAll : kSome};
+  const Fill fill = kinds ? kShift : nvec == tpr * (per / ve) ? kAll : kSome;
+  return Shape{per, tpr, tpr * groups, groups, kinds ? kinds : 1, fill};
 }
 
 // CTAs for `rows` rows in batches of `n` rows a group: as many as are resident
 // at once, or as there are batches; as many for each kind.
 int grid_for(int64_t rows, const Shape& s, int n) {
-  const int64_t each = (rows + s.kinds - 1) / s.kinds, batches = (each + (int64_t)s.groups * n - 1) / ((int64_t)s.groups * n);
+  const int64_t each = (rows + s.kinds - 1) / s.kinds, batch = (int64_t)s.groups * n;
+  const int64_t batches = (each + batch - 1) / batch;
   const int64_t most = 148 * ctas_of(s.per) / s.kinds;
   return (int)(batches < most ? batches : most) * s.kinds;
 }

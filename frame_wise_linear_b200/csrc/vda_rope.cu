@@ -241,10 +241,10 @@ cudaError_t run(RopeArgs& a, int pairing, cudaStream_t st) {
 
 cudaError_t launch_rope(const vda_rope_problem& p, const void* Q, const void* K, const float* positions, void* Qo,
                         void* Ko, bool backward, cudaStream_t st) {
+  if (!p.B || !p.T || !p.height || !p.width || p.H_q + p.H_k == 0) return cudaSuccess;
   RopeArgs a{};
   a.N = (uint32_t)((int64_t)p.T * p.height * p.width);   // B N is below 2^31
   a.tokens = (uint32_t)p.B * a.N;
-  if (a.tokens == 0 || p.H_q + p.H_k == 0) return cudaSuccess;
   a.in[0] = Q;
   a.in[1] = K;
   a.out[0] = Qo;

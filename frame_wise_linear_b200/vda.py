@@ -392,9 +392,8 @@ def make_rope_problem(B, T, height, width, H_q, H_k, d, axes, dtype, layout=VDA_
                       ld_q=0, ld_k=0, ld_qr=0, ld_kr=0) -> vda_rope_problem:
     """`axes` = (d_t, d_y, d_x): the channels that turn by time, height and width."""
     d_t, d_y, d_x = axes
-    vec = ctypes.c_double * 3
-    return vda_rope_problem(ld_q, ld_k, ld_qr, ld_kr, theta, vec(*pos0), vec(*step), B, T, height, width, H_q, H_k, d,
-                            d_t, d_y, d_x, dtype, layout, pairing, 0)
+    return vda_rope_problem(ld_q, ld_k, ld_qr, ld_kr, theta, tuple(pos0), tuple(step), B, T, height, width, H_q, H_k,
+                            d, d_t, d_y, d_x, dtype, layout, pairing, 0)
 
 
 def make_checkpoint_problem(rows, D, dtype, ld=0) -> vda_checkpoint_problem:
