@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
       for (int j = 0; j < kSize / 2; ++j) xh.p[j] = mul2(xh.p[j], both(rstd[r]));
     }
   };
+  // The last sum may be launched from here on; it waits for this grid's end.
+  cudaTriggerProgrammaticLaunchCompletion();
   int64_t row0 = p.cta * span;
   fetch(0, row0, std::false_type());
   async_commit();
