@@ -11,17 +11,24 @@ cudaError_t launch_pass(const NormArgs& a, const Shape& s, int grid, cudaStream_
 
 // dW and db from the CTAs' partial sums [parts][2 D]: 32 columns a block,
 // thread (x, y) adds rows y, y + 32, ...; then a warp the 32 sums of a column.
-// The rows come from L2; there are at most 296 of them, so a thread has ten
-// loads, all on their way at once.
+// The rows come from L2, and there are at most kMostParts of them: a thread's
+// loads are all on their way before the first is added (296 rows of 2002
+// columns: 4.6 us one after the other).
+constexpr int kMostParts = 320;
+static_assert(kMostParts >= 148 * ctas_of(16) && kMostParts % 32 == 0, "every CTA's row is added");
 __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* partial, int parts, int D, float* dW, float* db) {
   __shared__ float sh[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
-  float v = 0.f;
   cudaGridDependencySynchronize();
-  if (c < 2 * D) {
-#pragma unroll 10
-    for (int i = y; i < parts; i += 32) v += partial[(int64_t)i * 2 * D + c];
+  float part[kMostParts / 32];
+#pragma unroll
+  for (int j = 0; j < kMostParts / 32; ++j) {
+    const int i = y + j * 32;
+    part[j] = c < 2 * D && i < parts ? partial[(int64_t)i * 2 * D + c] : 0.f;
   }
+  float v = part[0];
+#pragma unroll
+  for (int j = 1; j < kMostParts / 32; ++j) v += part[j];
   sh[y][x] = v;
   __syncthreads();
   // Warp y adds column y's 32 sums.
