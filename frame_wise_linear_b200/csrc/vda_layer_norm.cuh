@@ -110,7 +110,7 @@ constexpr int kThreads = 256;   // of a CTA at most, and the ring's stride
 //   aligned vector, and the shift repeats every `kinds` rows; a CTA takes rows
 //   of one kind, so that its threads keep their columns.  The first and last
 //   vector of a row hold elements of its neighbours, too: read and left alone.
-//   45360 x 1001 bf16: forward 64 us, backward 92 us; by single elements 126
+//   45360 x 1001 bf16: forward 65 us, backward 82 us; by single elements 126
 //   and 190 us.
 enum Fill { kAll, kSome, kShift };
 
@@ -119,6 +119,7 @@ enum Fill { kAll, kSome, kShift };
 template <int VE, int NV, int F>
 struct Place {
   int t, group, groups, tpr, nvec, lanes, warps, lane, warp, first, D, shift, kind, kinds;
+  uint32_t has_bits, whole_bits;   // by vector
   int64_t rows, cta, ctas;   // rows of this CTA's kind, its place among the CTAs that share them
   __device__ __forceinline__ explicit Place(const NormArgs& a) {
     tpr = a.tpr;
@@ -146,18 +147,24 @@ struct Place {
     lane = threadIdx.x & 31;
     warp = threadIdx.x >> 5;
     first = warp / warps * warps;   // the row's first warp
+    has_bits = whole_bits = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      has_bits |= (vec(k) < nvec ? 1u : 0u) << k;
+      whole_bits |= (F == kShift ? col(k) >= 0 && col(k) + VE <= D : vec(k) < nvec) ? 1u << k : 0u;
+    }
   }
   // Row i of this kind among all rows.
   __device__ __forceinline__ int64_t real(int64_t i) const { return F == kShift ? i * kinds + kind : i; }
   __device__ __forceinline__ int vec(int k) const { return t + k * tpr; }
   __device__ __forceinline__ int col(int k) const { return vec(k) * VE - shift; }
-  __device__ __forceinline__ bool has(int k) const { return F == kAll || vec(k) < nvec; }
+  __device__ __forceinline__ bool has(int k) const { return F == kAll || (has_bits >> k & 1); }
   // Element i of vector k is one of the row's; all of vector k's are.
   __device__ __forceinline__ bool in(int k, int i) const {
     return F == kShift ? (unsigned)(col(k) + i) < (unsigned)D : has(k);
   }
   __device__ __forceinline__ bool whole(int k) const {
-    return F == kShift ? col(k) >= 0 && col(k) + VE <= D : has(k);
+    return F == kAll || (whole_bits >> k & 1);
   }
   // Columns of the row among n that start at column c.
   __device__ __forceinline__ int columns(int c, int n) const {
