@@ -326,6 +326,7 @@ vda_status vda_merge_project(const vda_merge_problem* p, const void* O_lin, cons
  * condition, so there is no error word and vda_sync_status does not apply to
  * their workspace.  (3) Sizes may be zero: such a call checks its arguments,
  * reads no tensor and returns VDA_OK (gradients of shared weights become 0).
+ * (vda_backward_from_checkpoint, at the end, is like vda_backward in all three.)
  * Every call is asynchronous on `stream`, allocates nothing, and may be
  * captured into a CUDA graph.  Errors on the host, before anything is
  * enqueued: VDA_ERR_INVALID_ARG (sizes, strides, unknown types, NULL or
