@@ -269,19 +269,19 @@ struct Batch {
       }
     }
   }
-  // The thread's vector k of row r, zeros where it has no element.
+  // The thread's vector k of row r.  Where it has no element: zeros, or `none`
+  // in a shifted row's vector.
   template <int F>
-  __device__ __forceinline__ Pack<T, VE> get(int buf, int r, int k, const T* row, const Place<VE, NV, F>& p) const {
+  __device__ __forceinline__ Pack<T, VE> get(int buf, int r, int k, const T* row, const Place<VE, NV, F>& p,
+                                             T none = T(0.f)) const {
     Pack<T, VE> q;
     if constexpr (F != kAll) q.zero();
     if (p.has(k)) q.load(kAsync ? slot(buf, r, k) : row + p.col(k));
     if constexpr (F == kShift) {
       if (!p.whole(k)) {
-        Pack<T, VE> none;
-        none.zero();
 #pragma unroll
         for (int i = 0; i < VE; ++i)
-          if (!p.in(k, i)) q.e[i] = none.e[i];
+          if (!p.in(k, i)) q.e[i] = none;
       }
     }
     return q;
@@ -304,13 +304,15 @@ __device__ __forceinline__ void get_chunk(const Batch<T, VE, NV, kRows, kAsync>&
   }
 }
 
-// The same plus `by`.
+// The same plus `by`.  A shifted row's vector has -by in the type where it has
+// no element, for a difference next to 0: 0 + by, times rstd, overflows for
+// constant rows from 3.4e38 sqrt(eps) up.
 template <typename T, int VE, int NV, int kRows, bool kAsync, int F>
 __device__ __forceinline__ void get_plus(const Batch<T, VE, NV, kRows, kAsync>& in, int buf, int r, const T* row,
                                          const Place<VE, NV, F>& p, int c, float by, Chunk<VE>& out) {
 #pragma unroll
   for (int k = 0; k < kOf<VE>; ++k) {
-    const Pack<T, VE> q = in.get(buf, r, c * kOf<VE> + k, row, p);
+    const Pack<T, VE> q = in.get(buf, r, c * kOf<VE> + k, row, p, from_f32<T>(F == kShift ? -by : 0.f));
     if constexpr (VE > 1) {
 #pragma unroll
       for (int i = 0; i < VE; i += 2) out.p[i / 2] = plus2(q, i, both(by));

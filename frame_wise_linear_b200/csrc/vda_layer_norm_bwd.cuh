@@ -71,8 +71,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
       get_codes(inx, buf, r, X + x_at(row), p, sb[r], by, c, xh);
     } else {
       get_plus(inx, buf, r, X + x_at(row), p, c, -mean[r], xh);
+      // Where a vector is missing x is 0, and -mean rstd overflows for constant
+      // rows from 3.4e38 sqrt(eps) up.
 #pragma unroll
-      for (int j = 0; j < kSize / 2; ++j) xh.p[j] = mul2(xh.p[j], both(rstd[r]));
+      for (int j = 0; j < kSize / 2; ++j) {
+        const int k = VE > 1 ? c : 2 * c, k1 = VE > 1 ? c : 2 * c + 1;
+        const float2 rs = F != kSome ? both(rstd[r]) : make_float2(p.has(k) ? rstd[r] : 0.f, p.has(k1) ? rstd[r] : 0.f);
+        xh.p[j] = mul2(xh.p[j], rs);
+      }
     }
   };
   // The last sum may be launched from here on; it waits for this grid's end.
@@ -100,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV * VE)) norm_bwd_kernel(co
         if (!kWhole && at >= p.rows) continue;
         Chunk<VE> dy, xh;
         get(buf, r, row, 1.f, c, dy, xh);
-        // Where the thread has no element dy is 0: nothing is added.
+        // Where the thread has no element dy is 0 and xh finite: nothing is added.
 #pragma unroll
         for (int j = 0; j < kSize / 2; ++j) {
           const float2 t = mul2(dy.p[j], xh.p[j]);

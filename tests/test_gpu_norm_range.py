@@ -1,0 +1,77 @@
+"""Layer norm near float32's end: rows of one large value, at widths that leave threads or parts of vectors empty.
+
+Where a thread has no element of a row it holds zeros, and nothing that it computes from them may reach the row: at
+these magnitudes (0 - mean) rstd overflows, and a product of it with 0 is NaN.
+"""
+import numpy as np
+import pytest
+
+from oracle import token_oracle as o
+from token_testutil import U32, assert_close, code_of, dtype_of, f64, half_step, inside
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+BIG = 2.0 ** 119          # BIG / sqrt(EPS) is 2^129, beyond float32
+
+# Width, type, heads, elements between tokens beyond them: vectors that some threads lack, shifted vectors, single
+# elements.
+WIDTHS = [(8, "bf16", 1, 0), (24, "bf16", 1, 0), (1000, "bf16", 1, 0), (4, "f32", 1, 0), (1004, "f32", 1, 0),
+          (33, "bf16", 1, 0), (1001, "bf16", 1, 0), (1001, "f32", 1, 0), (7, "bf16", 1, 0), (7, "f32", 3, 0),
+          (77, "bf16", 2, 3), (1001, "f32", 1, 1), (8, "bf16", 5, 8)]
+
+
+@pytest.mark.parametrize("D,dtype,heads,pad", WIDTHS)
+@pytest.mark.parametrize("tokens", [3, 4000])
+def test_gradients_of_large_constant_rows(D, dtype, heads, pad, tokens):
+    """x = mean exactly, so xh = 0: dX = rstd (g - mean(g)), dW = 0.
+
+    The sums of g xh are sums of zeros, and the bound is that of test_gpu_norm.py with |xh| = 0 and no error in it:
+    g one rounding, its mean at most 45 roundings of the mean of |g| and the division's, the difference and the
+    product one each.  db: 3 roundings a batch of rows would be few; every column's term passes at most `rows`
+    additions, which is what is allowed.
+    """
+    import torch
+    from frame_wise_linear_b200 import vda
+    rng = np.random.default_rng(D + heads)
+    dt, width = dtype_of(dtype), heads * D
+    ld, rows = width + pad, tokens * heads
+    X, _ = inside(tokens, width, ld, dt, 0.0)
+    sign = rng.choice([-1.0, 1.0], (tokens, heads, 1))
+    X.copy_(torch.from_numpy(np.broadcast_to(BIG * sign, (tokens, heads, D)).reshape(tokens, width).copy()).cuda())
+    dY, _ = inside(tokens, width, ld, dt, 0.0)
+    dY.copy_(torch.from_numpy(rng.normal(size=(tokens, width))).cuda())
+    W = torch.from_numpy(rng.normal(1.0, 0.3, D)).float().cuda()
+    mean = X.as_strided((tokens, heads), (ld, D)).float().reshape(rows).contiguous()
+    rstd = torch.full((rows,), EPS ** -0.5, device="cuda")
+    p = vda.make_norm_problem(tokens, D, code_of(dtype), heads=heads, eps=EPS, ld_x=ld if pad else 0,
+                              ld_y=ld if pad else 0)
+    dX, _ = inside(tokens, width, ld, dt, 7.0)
+    dW, db = torch.full((2, D), 7.0, device="cuda")
+    ws = torch.full((vda.vda_layer_norm_backward_workspace_size(p),), 255, dtype=torch.uint8, device="cuda")
+    vda.vda_layer_norm_backward(p, dY, X, mean, rstd, W, dX, dW, db, ws)
+    dy, w, r = f64(dY).reshape(rows, D), f64(W), f64(rstd)
+    ref, _, db_ref = o.layer_norm_backward(dy, np.zeros((rows, D)), r, w)
+    g = np.abs(dy * w)
+    err = r[:, None] * U32 * (6 * g + 50 * g.mean(1, keepdims=True))
+    assert_close(f64(dX).reshape(rows, D), ref, err + half_step(dt) * (np.abs(ref) + err), "dX")
+    assert bool((dW == 0).all())
+    assert_close(f64(db), db_ref, rows * U32 * np.abs(dy).sum(0), "db")
+
+
+@pytest.mark.parametrize("D,dtype", [(8, "bf16"), (16, "bf16"), (32, "bf16"), (4, "f32"), (16, "f32")])
+def test_forward_and_backward_of_large_constant_rows(D, dtype):
+    """A power of two of elements: the mean of a constant row is exact, y is the bias, and the gradients are finite."""
+    import torch
+    from frame_wise_linear_b200 import vda
+    n = 5
+    X = torch.full((n, D), BIG, device="cuda").to(dtype_of(dtype))
+    W, b = torch.full((D,), 2.0, device="cuda"), torch.arange(D, device="cuda").float()
+    p = vda.make_norm_problem(n, D, code_of(dtype), eps=EPS)
+    Y, (mean, rstd) = torch.empty_like(X), torch.empty(2, n, device="cuda")
+    vda.vda_layer_norm(p, X, W, b, Y, mean, rstd)
+    assert bool((mean == BIG).all()) and bool((Y == b.to(Y.dtype)).all())
+    dX, (dW, db) = torch.empty_like(X), torch.empty(2, D, device="cuda")
+    ws = torch.empty(vda.vda_layer_norm_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    vda.vda_layer_norm_backward(p, torch.ones_like(X), X, mean, rstd, W, dX, dW, db, ws)
+    assert bool((dX == 0).all()) and bool((dW == 0).all()) and bool((db == n).all())
