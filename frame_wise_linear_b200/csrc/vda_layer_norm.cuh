@@ -498,7 +498,9 @@ template <int kPass, typename T, int VE, int NV>
 cudaError_t run_fill(const NormArgs& a, const Shape& s, int* parts, cudaStream_t st) {
   if constexpr (VE > 1) {
     if (s.fill == kAll) return run_shape<kPass, T, VE, NV, kAll>(a, s, parts, st);
-    if constexpr (kPass != kForwardCodes) {
+    // Shifted rows have four vectors at least, and with a fifth for the shift more
+    // than the 32 bf16 that 8 a thread are for.
+    if constexpr (kPass != kForwardCodes && VE * NV * (int)sizeof(T) > 16) {
       if (s.fill == kShift) return run_shape<kPass, T, VE, NV, kShift>(a, s, parts, st);
     }
   }

@@ -24,7 +24,6 @@ constexpr int kBlock = 32;   // elements that share a scale
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(uint8_t x) { return (float)x; }
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
 template <>
@@ -41,7 +40,7 @@ template <> struct RawOf<8> { using type = uint2; };
 template <> struct RawOf<16> { using type = uint4; };
 
 // VE consecutive elements of type T as they are stored: one load or store of
-// VE * sizeof(T) bytes (2 to 16), whose address is a multiple of that.
+// VE * sizeof(T) bytes (1 to 16), whose address is a multiple of that.
 template <typename T, int VE>
 struct Pack {
   using Raw = typename RawOf<VE * (int)sizeof(T)>::type;
