@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -212,27 +213,59 @@ def _ptr(x) -> int | None:
     return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
+_get_device = None
+
+
+def _current_device() -> int | None:
+    """torch's current device (None without torch or CUDA), without the checks of each call that torch makes."""
+    global _get_device
+    if _get_device is None:
+        torch = sys.modules.get("torch")
+        if torch is None or not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _get_device()
+
+
 _raw_stream = None
 
 
-def _current_stream() -> int:
+def _current_stream(device=None) -> int:
     """torch's current stream of the current device, without making a Stream object where torch offers that."""
     global _raw_stream
     if _raw_stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         torch.cuda.init()
-        _raw_stream = (lambda: raw(torch._C._cuda_getDevice())) if raw else \
-            (lambda: torch.cuda.current_stream().cuda_stream)
-    return _raw_stream()
+        _raw_stream = raw if raw else (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(_current_device() if device is None else device)
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device=None) -> int | None:
     if stream is None:
-        return _current_stream()
+        return _current_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _refuse(x, here):
+    at = x.get_device()
+    raise ValueError("tensors must be CUDA tensors" if at < 0 else
+                     f"a tensor is on CUDA device {at}, the current device is {here}")
+
+
+def _on_device(stream, *tensors):
+    """The addresses of tensors on the current device (None and addresses as they are), and the stream's handle.
+
+    The kernels run on the current device; memory of the host or of another
+    device would fault there, so such a tensor raises a ValueError.
+    """
+    here = _current_device()
+    ptrs = [x if x is None or x.__class__ is int else x.data_ptr() if x.get_device() == here else _refuse(x, here)
+            for x in tensors]
+    return ptrs, _stream(stream, here)
 
 
 def vda_workspace_size(problem: vda_problem) -> int:
@@ -381,6 +414,7 @@ def vda_merge_project(tokens, K, D, O_lin, W_lin, O_sm, W_sm, Y, workspace, stre
 
 # ---------------------------------------------------------------------------
 # Token operators: layer norm, rotary positions, 8-bit checkpoints
+# (tensors must be on the current CUDA device: ValueError otherwise)
 # ---------------------------------------------------------------------------
 
 def make_norm_problem(tokens, D, dtype, heads=1, w_dtype=VDA_DTYPE_F32, eps=1e-6, ld_x=0, ld_y=0) -> vda_norm_problem:
@@ -403,8 +437,8 @@ def make_checkpoint_problem(rows, D, dtype, ld=0) -> vda_checkpoint_problem:
 def vda_layer_norm(problem, X, W, bias, Y, mean=None, rstd=None, codes=None, scales=None, stream=None,
                    check=True) -> int:
     """Y = (X - mean) rstd W + bias per row; codes and scales: the normalised rows as an 8-bit checkpoint."""
-    s = load().vda_layer_norm(ctypes.byref(problem), _ptr(X), _ptr(W), _ptr(bias), _ptr(Y), _ptr(mean), _ptr(rstd),
-                              _ptr(codes), _ptr(scales), _stream(stream))
+    ptrs, st = _on_device(stream, X, W, bias, Y, mean, rstd, codes, scales)
+    s = load().vda_layer_norm(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_layer_norm")
     return s
@@ -412,8 +446,8 @@ def vda_layer_norm(problem, X, W, bias, Y, mean=None, rstd=None, codes=None, sca
 
 def vda_layer_norm_from_checkpoint(problem, codes, scales, W, bias, Y, stream=None, check=True) -> int:
     """Y again from the checkpoint that vda_layer_norm left."""
-    s = load().vda_layer_norm_from_checkpoint(ctypes.byref(problem), _ptr(codes), _ptr(scales), _ptr(W), _ptr(bias),
-                                              _ptr(Y), _stream(stream))
+    ptrs, st = _on_device(stream, codes, scales, W, bias, Y)
+    s = load().vda_layer_norm_from_checkpoint(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_layer_norm_from_checkpoint")
     return s
@@ -430,8 +464,8 @@ def vda_layer_norm_backward(problem, dY, X, mean, rstd, W, dX, dW, dbias, worksp
                             workspace_bytes=None, check=True) -> int:
     """dX, dW, dbias (the last two float32, either may be None) of sum(dY * Y)."""
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    s = load().vda_layer_norm_backward(ctypes.byref(problem), _ptr(dY), _ptr(X), _ptr(mean), _ptr(rstd), _ptr(W),
-                                       _ptr(dX), _ptr(dW), _ptr(dbias), _ptr(workspace), wb, _stream(stream))
+    ptrs, st = _on_device(stream, dY, X, mean, rstd, W, dX, dW, dbias, workspace)
+    s = load().vda_layer_norm_backward(ctypes.byref(problem), *ptrs, wb, st)
     if check:
         _check(s, "vda_layer_norm_backward")
     return s
@@ -441,9 +475,8 @@ def vda_layer_norm_backward_from_checkpoint(problem, dY, codes, scales, rstd, W,
                                             workspace_bytes=None, check=True) -> int:
     """As vda_layer_norm_backward, from the 8-bit checkpoint of the normalised rows instead of X and mean."""
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    s = load().vda_layer_norm_backward_from_checkpoint(ctypes.byref(problem), _ptr(dY), _ptr(codes), _ptr(scales),
-                                                       _ptr(rstd), _ptr(W), _ptr(dX), _ptr(dW), _ptr(dbias),
-                                                       _ptr(workspace), wb, _stream(stream))
+    ptrs, st = _on_device(stream, dY, codes, scales, rstd, W, dX, dW, dbias, workspace)
+    s = load().vda_layer_norm_backward_from_checkpoint(ctypes.byref(problem), *ptrs, wb, st)
     if check:
         _check(s, "vda_layer_norm_backward_from_checkpoint")
     return s
@@ -451,8 +484,8 @@ def vda_layer_norm_backward_from_checkpoint(problem, dY, codes, scales, rstd, W,
 
 def vda_rope(problem, Q, K, positions, Q_rot, K_rot, stream=None, check=True) -> int:
     """Q, K turned by their positions over (time, height, width); positions: float32 [B, N, 3], or None (the grid)."""
-    s = load().vda_rope(ctypes.byref(problem), _ptr(Q), _ptr(K), _ptr(positions), _ptr(Q_rot), _ptr(K_rot),
-                        _stream(stream))
+    ptrs, st = _on_device(stream, Q, K, positions, Q_rot, K_rot)
+    s = load().vda_rope(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_rope")
     return s
@@ -460,8 +493,8 @@ def vda_rope(problem, Q, K, positions, Q_rot, K_rot, stream=None, check=True) ->
 
 def vda_rope_backward(problem, dQ_rot, dK_rot, positions, dQ, dK, stream=None, check=True) -> int:
     """The gradients with respect to Q, K from those with respect to Q_rot, K_rot."""
-    s = load().vda_rope_backward(ctypes.byref(problem), _ptr(dQ_rot), _ptr(dK_rot), _ptr(positions), _ptr(dQ),
-                                 _ptr(dK), _stream(stream))
+    ptrs, st = _on_device(stream, dQ_rot, dK_rot, positions, dQ, dK)
+    s = load().vda_rope_backward(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_rope_backward")
     return s
@@ -469,7 +502,8 @@ def vda_rope_backward(problem, dQ_rot, dK_rot, positions, dQ, dK, stream=None, c
 
 def vda_checkpoint_pack(problem, X, codes, scales, stream=None, check=True) -> int:
     """X [rows, D] as e4m3 codes and a power-of-two scale byte per 32 neighbours of a row."""
-    s = load().vda_checkpoint_pack(ctypes.byref(problem), _ptr(X), _ptr(codes), _ptr(scales), _stream(stream))
+    ptrs, st = _on_device(stream, X, codes, scales)
+    s = load().vda_checkpoint_pack(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_checkpoint_pack")
     return s
@@ -477,7 +511,8 @@ def vda_checkpoint_pack(problem, X, codes, scales, stream=None, check=True) -> i
 
 def vda_checkpoint_unpack(problem, codes, scales, X, stream=None, check=True) -> int:
     """The values that codes and scales stand for, in the problem's type."""
-    s = load().vda_checkpoint_unpack(ctypes.byref(problem), _ptr(codes), _ptr(scales), _ptr(X), _stream(stream))
+    ptrs, st = _on_device(stream, codes, scales, X)
+    s = load().vda_checkpoint_unpack(ctypes.byref(problem), *ptrs, st)
     if check:
         _check(s, "vda_checkpoint_unpack")
     return s
@@ -497,10 +532,9 @@ def vda_backward_from_checkpoint(problem, checkpoints, dO, dQ, dK, dV, dG, dK_tx
     pairs = [(None, None) if c is None else c for c in checkpoints]
     if len(pairs) != 6:
         raise ValueError("checkpoints holds six entries: Q, K, V, G, K_txt, V_txt")
-    arr = (vda_checkpoint * 6)(*[vda_checkpoint(_ptr(a), _ptr(b)) for a, b in pairs])
-    s = load().vda_backward_from_checkpoint(ctypes.byref(problem), arr, _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV),
-                                            _ptr(dG), _ptr(dK_txt), _ptr(dV_txt), _ptr(workspace), wb,
-                                            _stream(stream))
+    arr = (vda_checkpoint * 6)(*[vda_checkpoint(*_on_device(0, a, b)[0]) for a, b in pairs])
+    ptrs, st = _on_device(stream, dO, dQ, dK, dV, dG, dK_txt, dV_txt, workspace)
+    s = load().vda_backward_from_checkpoint(ctypes.byref(problem), arr, *ptrs, wb, st)
     if check:
         _check(s, "vda_backward_from_checkpoint")
     return s
