@@ -313,6 +313,8 @@ def vda_host_workspace_size(problem: vda_problem) -> int:
 
 
 def _nbytes(x) -> int:
+    if x is None:
+        return 0
     if isinstance(x, int):
         return 1 << 62
     return x.numel() * x.element_size()

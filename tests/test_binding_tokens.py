@@ -68,3 +68,14 @@ def test_tensors_of_another_device_refused(which, monkeypatch):
         a[i] = _On(1)
         with pytest.raises(ValueError, match="device 1"):
             call(*a)
+
+
+@pytest.mark.parametrize("fn", ["vda_layer_norm_backward", "vda_layer_norm_backward_from_checkpoint"])
+def test_no_workspace_is_an_argument_like_others(fn):
+    """None for the workspace, its size not given: refused by the library where weight gradients are wanted, and
+    taken where there are none (here with no tokens, so that nothing runs)."""
+    call = getattr(vda, fn)
+    some, none = vda.make_norm_problem(4, 64, F32), vda.make_norm_problem(0, 64, F32)
+    for dw, db in ((OK, OK), (OK, None), (None, OK)):
+        assert call(some, OK, OK, OK, OK, OK, OK, dw, db, None, stream=0, check=False) == vda.VDA_ERR_WORKSPACE
+    assert call(none, None, None, None, None, None, None, None, None, None, stream=0, check=False) == vda.VDA_OK
