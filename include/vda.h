@@ -376,8 +376,10 @@ vda_status vda_layer_norm_from_checkpoint(const vda_norm_problem* p, const void*
  * vda_layer_norm_backward_workspace_size() bytes (256-byte aligned; contents
  * on entry do not matter; two calls that may overlap, or two graphs that may
  * run at once, need one each).  The sums are added in an order that depends
- * on the sizes alone, so equal calls give equal bits.  dX may be X, or dY
- * where ld_x == ld_y; other overlaps are not allowed. */
+ * on the sizes, the strides and the tensors' places within 16 bytes, never on
+ * timing: calls that agree in these give equal bits, others the same sums
+ * rounded otherwise.  dX may be X, or dY where ld_x == ld_y; other overlaps are
+ * not allowed. */
 vda_status vda_layer_norm_backward_workspace_size(const vda_norm_problem* p, size_t* bytes);
 vda_status vda_layer_norm_backward(const vda_norm_problem* p, const void* dY, const void* X, const float* mean,
                                    const float* rstd, const void* W, void* dX, float* dW, float* dbias,

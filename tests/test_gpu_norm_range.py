@@ -75,3 +75,34 @@ def test_forward_and_backward_of_large_constant_rows(D, dtype):
     ws = torch.empty(vda.vda_layer_norm_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
     vda.vda_layer_norm_backward(p, torch.ones_like(X), X, mean, rstd, W, dX, dW, db, ws)
     assert bool((dX == 0).all()) and bool((dW == 0).all()) and bool((db == n).all())
+
+
+@pytest.mark.parametrize("D,dtype,place", [(4096, "bf16", 0), (1001, "bf16", 3), (1001, "f32", 1), (72, "bf16", 0)])
+def test_equal_bits_at_equal_places(D, dtype, place):
+    """Buffers elsewhere, but at the same place within 16 bytes, give the same bits, whatever else runs."""
+    import torch
+    from frame_wise_linear_b200 import vda
+    n, dt = 3001, dtype_of(dtype)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    x, dy = (torch.randn(n, D, device="cuda", generator=g).to(dt) for _ in range(2))
+    W = torch.rand(D, device="cuda", generator=g)
+    p = vda.make_norm_problem(n, D, code_of(dtype), eps=EPS)
+    ws = torch.empty(vda.vda_layer_norm_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    side, big, want = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda"), None
+    for i in range(6):
+        at = place + i * (16 // x.element_size())
+        X, dY, dX = (inside(n, D, D, dt, 0.0, at)[0] for _ in range(3))
+        X.copy_(x)
+        dY.copy_(dy)
+        mean, rstd = torch.empty(2, n, device="cuda")
+        dW, db = torch.empty(2, D, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(i):
+                big @ big
+        vda.vda_layer_norm(p, X, W, None, dX, mean, rstd)
+        y = dX.clone()
+        vda.vda_layer_norm_backward(p, dY, X, mean, rstd, W, dX, dW, db, ws)
+        got = [y, mean, rstd, dX, dW, db]
+        want = want or [t.clone() for t in got]
+        assert all(torch.equal(a, c) for a, c in zip(got, want)), i
