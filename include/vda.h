@@ -431,7 +431,8 @@ typedef struct vda_rope_problem {
 vda_status vda_rope(const vda_rope_problem* p, const void* Q, const void* K, const float* positions, void* Q_rot,
                     void* K_rot, void* stream);
 /* dQ_rot, dK_rot (strides ld_qr, ld_kr) -> dQ, dK (strides ld_q, ld_k): the
- * turn the other way, which is also the exact inverse of vda_rope. */
+ * turn the other way, which is also the inverse of vda_rope up to the
+ * outputs' rounding. */
 vda_status vda_rope_backward(const vda_rope_problem* p, const void* dQ_rot, const void* dK_rot,
                              const float* positions, void* dQ, void* dK, void* stream);
 
