@@ -342,6 +342,9 @@ vda_status vda_merge_project(const vda_merge_problem* p, const void* O_lin, cons
  *     xh = (x - m) r,  y = xh * W + bias
  * dtype: X, Y, dY, dX (float32 or bfloat16); w_dtype: W, bias.  dW and dbias
  * are float32 (sums over all rows; the caller rounds them if it wants to).
+ * Range: a row's sum and its sum of squared differences are float32, too, so
+ * rows are normalised while both stay below 3.4e38 (elements up to 10^17 at
+ * any width); beyond, r is 0 or the row is NaN.
  * tokens in [0, 2^31), heads in [1, 65536], D in [1, 8192], eps finite, > 0.
  * ld_x: elements from one token to the next in X and dX; ld_y: in Y and dY;
  * 0 means heads * D, else at least that and below 2^31 (a slice of a wider

@@ -77,6 +77,29 @@ def test_forward_and_backward_of_large_constant_rows(D, dtype):
     assert bool((dX == 0).all()) and bool((dW == 0).all()) and bool((db == n).all())
 
 
+@pytest.mark.parametrize("D,dtype", [(8192, "bf16"), (8192, "f32"), (4096, "bf16"), (1001, "f32"), (77, "bf16")])
+def test_range_of_rows(D, dtype):
+    """Elements of 10^17 are normalised at any width; where the squares pass float32 r is 0 and Y the bias, and where
+    the sum does the row is NaN.  The sizes are powers of two: within the range Y is off by the statistics' bound of
+    test_gpu_norm_forms.py with X R <= 2 sqrt(2), one multiply-add and the rounding to its type."""
+    import torch
+    from frame_wise_linear_b200 import vda
+    dt = dtype_of(dtype)
+    rng = np.random.default_rng(D)
+    sign = np.where(rng.permutation(D) % 2, 1.0, -1.0)
+    x = np.stack([sign * 2.0 ** 56, sign * 2.0 ** 90, np.full(D, 2.0 ** 127)])      # 2^56 = 0.72e17
+    X = torch.from_numpy(x).to(dt).cuda()
+    b = torch.full((D,), 0.5, device="cuda")
+    p = vda.make_norm_problem(3, D, code_of(dtype), eps=EPS)
+    Y, (mean, rstd) = torch.empty_like(X), torch.empty(2, 3, device="cuda")
+    vda.vda_layer_norm(p, X, None, b, Y, mean, rstd)
+    ref = o.layer_norm(x[:1], None, f64(b), EPS)[0]
+    err = U32 * (32 * 3 + 2 * (16 + 96 + 3)) + 2 * U32
+    assert_close(f64(Y[:1]), ref, err * 1.01 + half_step(dt) * (np.abs(ref) + err))
+    assert float(rstd[1]) == 0 and bool((Y[1] == 0.5).all())
+    assert bool(torch.isnan(Y[2]).all())
+
+
 @pytest.mark.parametrize("D,dtype,place", [(4096, "bf16", 0), (1001, "bf16", 3), (1001, "f32", 1), (72, "bf16", 0)])
 def test_equal_bits_at_equal_places(D, dtype, place):
     """Buffers elsewhere, but at the same place within 16 bytes, give the same bits, whatever else runs."""
