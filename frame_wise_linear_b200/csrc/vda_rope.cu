@@ -71,8 +71,9 @@ __device__ __forceinline__ float2 turn_of(const RopeArgs& a, uint32_t token, int
 //   Else: pair j is channels (2 j, 2 j + 1); a unit is VE neighbours, or (kPair)
 //   one pair loaded as single elements, or the last channel of an odd d.
 // Four CTAs of an SM: with the 80 registers that the compiler would take 8191
-// packed tokens take 20.6 us against 18.9, with five CTAs it spills (31 us).
-// 768p: 219 us, 1.03 of the copy rate.
+// packed tokens take 20.6 us against 18.9, with five CTAs it spills (31 us).  At
+// four the 16-byte form of kHalves spills, too: 40 bytes a thread, 48 read back.
+// 768p: neighbours 223 us, 1.02 of the copy rate; halves 235 us, 0.96.
 template <typename T, int VE, bool kHalves, bool kPair>
 __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int NP = kHalves ? VE : (kPair ? 1 : VE / 2);   // pairs of a unit
