@@ -17,9 +17,9 @@
 // let the chains of their sums overlap, and share the barrier of a row's
 // warps.  Next to HBM the instructions count (a row of 4096 bf16 has 550 ns on
 // its SM in the backward, and the clock falls under the power cap), hence
-// float32 in pairs and bf16 added to float32 as it is.  45360 x 4096 bf16:
-// forward 118 us (0.96 of the copy rate, 0.89 in a long run), backward 188 us
-// (0.90; 0.84).
+// float32 in pairs and bf16 added to float32 as it is.  45360 x 4096 bf16, in a
+// run of calls: forward 123 to 128 us by the box (0.92 to 0.89 of the copy rate),
+// backward 190 to 201 us (0.90 to 0.85).
 //
 // The row's sums: shuffles within a warp, and where a row has several warps
 // one exchange through shared memory with one barrier a batch.  In the forward
@@ -110,8 +110,10 @@ constexpr int kThreads = 256;   // of a CTA at most, and the ring's stride
 //   aligned vector, and the shift repeats every `kinds` rows; a CTA takes rows
 //   of one kind, so that its threads keep their columns.  The first and last
 //   vector of a row hold elements of its neighbours, too: read and left alone.
-//   45360 x 1001 bf16: forward 65 us, backward 82 us; by single elements 126
-//   and 190 us.
+//   Every vector is tested for that, and the forward's squares element by
+//   element: 27 and 37 instructions of a warp for 32 elements, where whole
+//   vectors take 13 and 19, and they are what bounds it.  45360 x 1001 bf16:
+//   forward 67 us, backward 84 us; by single elements 126 and 190 us.
 enum Fill { kAll, kSome, kShift };
 
 // What a thread is in its CTA, and which columns it holds: vectors t + k tpr,
@@ -390,7 +392,10 @@ __device__ __forceinline__ void get_codes(const Batch<uint8_t, VE, NV, kRows, kA
 // CTAs of an SM that the kernels are compiled for, by the elements a thread
 // holds: two, with up to 128 registers a thread (with three the sums of a batch
 // spill: 45360 x 4096 bf16 forward 190 us against 148 at the time, backward 234
-// against 205), or one with twice the elements.
+// against 205), or one with twice the elements.  These spill all the same: the
+// forward of four shifted bf16 rows (12 bytes a thread), and of the single
+// elements the float32 forward with 32 of them (16 bytes), the backward from
+// codes with 16 or 32 (300 and 560) and y again with 32 (88).
 constexpr int ctas_of(int per) { return per == 32 ? 1 : 2; }
 
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
