@@ -5,10 +5,16 @@
 // Both directions are one pass over the data, bound by HBM: element size + 1
 // + 1/32 bytes an element.  Three forms, by alignment alone:
 //   - rows of 16-byte vectors: eight neighbouring lanes (float32) or four (bf16)
-//     hold a block, 16 bytes each, and find its largest magnitude by shuffles;
+//     hold a block, 16 bytes each, and find its largest magnitude by shuffles
+//     (1451520 x 128 bf16, both directions: 185 to 190 us, 0.93 to 0.90 of the
+//     copy rate);
 //   - dense rows at any alignment (odd widths): a CTA's blocks are one stretch of
-//     memory, copied through shared memory 16 bytes at a time on both sides;
-//   - rows with gaps at any alignment: one element a lane, a warp a block.
+//     memory, copied through shared memory 16 bytes at a time on both sides.
+//     Elements pass shared memory one by one and codes byte by byte, 42 and 29
+//     instructions of a warp for 32 bf16 elements, which bound it (45360 x 4090
+//     bf16, both directions: 414 us, 0.41; 22680 x 4095 float32: 231 us, 0.62);
+//   - rows with gaps at any alignment: one element a lane, a warp a block (45360 x
+//     4090 bf16 with rows 4091 apart: 1245 us, 0.14).
 #include "vda_internal.cuh"
 #include "vda_tokops.cuh"
 

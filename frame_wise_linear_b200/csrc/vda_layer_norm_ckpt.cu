@@ -1,4 +1,9 @@
 // Layer norm from the 8-bit normalised rows: the backward, and y again.
+//
+// 45360 x 4096 bf16: 191 and 101 us, 0.75 and 0.85 of the copy rate, bound by the
+// instructions that decode next to HBM.  45360 x 1001 bf16: 131 and 68 us, 0.27
+// and 0.31, 59 and 27 instructions of a warp for 32 elements: a shifted vector may
+// hold elements of two blocks, so each pair takes its own scales.
 #include "vda_layer_norm_bwd.cuh"
 
 namespace vda {
