@@ -407,8 +407,8 @@ vda_status vda_layer_norm_backward_from_checkpoint(const vda_norm_problem* p, co
  * axis (a later part of a long video starts at pos0[0]; step scales an axis),
  * or, for packed sequences, `positions`, float32 [B, N, 3] on the device
  * (pos0 and step are then not read; a position that is not finite gives NaN).
- * Angles are formed in double: positions to 10^6 and beyond are as exact as
- * near ones.  Q: H_q heads, K: H_k heads (either may be 0 with NULL
+ * Angles are formed in double: positions to 10^8 are as exact as near ones (an
+ * angle beyond double's range gives NaN).  Q: H_q heads, K: H_k heads (either may be 0 with NULL
  * pointers); dtype float32 or bfloat16.  layout VDA_LAYOUT_BTNHD:
  * [B, N, H, d], where ld_q, ld_k (Q, K) and ld_qr, ld_kr (the turned ones) give
  * the elements from one token to the next (0: H * d; else at least that and

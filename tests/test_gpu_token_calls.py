@@ -99,6 +99,31 @@ def test_channels_that_do_not_turn_keep_every_bit(d, axes, halves, dtype):
             assert torch.equal(y.view(ints)[..., sum(axes):], bits[..., sum(axes):])
 
 
+def test_far_positions():
+    """Positions of 10^8: the angle's double product is off by at most 3 half steps of 2^-53 of 1.6e7 turns, 3.3e-8
+    rad or half a u; the reference's angles have 64 bits."""
+    import torch
+    from frame_wise_linear_b200 import vda
+    if np.finfo(np.longdouble).nmant < 63:
+        pytest.skip("no wider type than double here")
+    d, axes, N = 128, (44, 42, 42), 50
+    x = torch.randn(1, N, 2, d, device="cuda")
+    y = torch.empty_like(x)
+    pos0 = (1e8, 1e8 - 7, -1e8)
+    p = vda.make_rope_problem(1, N, 1, 1, 2, 0, d, axes, vda.VDA_DTYPE_F32, layout=1, pos0=pos0)
+    vda.vda_rope(p, x, None, None, y, None)
+    L = np.longdouble
+    pos = np.stack([L(pos0[0]) + np.arange(N, dtype=L), np.full(N, L(pos0[1])), np.full(N, L(pos0[2]))], 1)
+    angle = np.concatenate([pos[:, [a]] * L(10000) ** (-np.arange(0, n, 2, dtype=L) / n) for a, n in enumerate(axes)], 1)
+    c, s = np.cos(angle)[:, None].astype(float), np.sin(angle)[:, None].astype(float)
+    a = f64(x)[0]
+    u, v = a[..., 0::2], a[..., 1::2]
+    bound = 9.5 * U32 * (np.abs(u) + np.abs(v))
+    got = f64(y)[0]
+    assert np.all(np.abs(got[..., 0::2] - (u * c - v * s)) <= bound + U32 * np.abs(got[..., 0::2]))
+    assert np.all(np.abs(got[..., 1::2] - (u * s + v * c)) <= bound + U32 * np.abs(got[..., 1::2]))
+
+
 class _Work:
     """The four groups of operators once, on tensors of one's own."""
 
