@@ -465,8 +465,10 @@ vda_status vda_checkpoint_unpack(const vda_checkpoint_problem* p, const void* co
  * from its bfloat16 tensor as rows of D = 128, in the problem's layout): the
  * gradients at the values that the checkpoints stand for.  `in`: six entries
  * in that order (the last two are not read when n_txt == 0).  workspace: at
- * least vda_backward_from_checkpoint_workspace_size() bytes, 256-byte aligned;
- * the error word, the other arguments and errors as for vda_backward. */
+ * least vda_backward_from_checkpoint_workspace_size() bytes, 256-byte aligned:
+ * vda_backward's and bfloat16 copies of the six tensors, which the call unpacks
+ * first (one workspace serves any number of layers in turn); the error word, the
+ * other arguments and errors as for vda_backward. */
 typedef struct vda_checkpoint {
   const void* codes;
   const void* scales;
